@@ -22,7 +22,7 @@ LIB_WAITTEST = os.path.join(HERE, "libfp8moe_waittest.so")
 LIB_ROLES = os.path.join(HERE, "libfp8moe_roles.so")
 VARIANTS = {LIB: [], LIB_WAITTEST: ["-DMOE_WAIT_TEST"], LIB_ROLES: ["-DMOE_ROLE_COUNTERS"]}
 SOURCES = ["moe_api.cu", "route.cu", "router_mma.cu", "permute.cu", "gemm.cu", "combine.cu",
-           "noalloc.cu", "dispatch.cu"]
+           "noalloc.cu", "dispatch.cu", "dense_gemm.cu", "int8.cu", "gated_ffn.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -54,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     if not force and not needs_build(lib):
         return lib
     cmd = [nvcc_path(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-cudart", "shared",
-           "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", *VARIANTS[lib], "-o", lib + ".tmp",
+           "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--threads", "0", *VARIANTS[lib], "-o", lib + ".tmp",
            *sources()]
     if ptxas_info:
         cmd.insert(1, "-Xptxas=-v")

@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,7 +28,7 @@ constexpr int kStatusDeviceCheck = -6;
 // where-codes stored next to the status (ws int[1]) to tell which kernel reported it
 enum Where : int {
   kWhereRoute = 1, kWherePermute = 2, kWhereGather = 3, kWhereGemm1 = 4, kWhereRequant = 5,
-  kWhereGemm2 = 6, kWhereCombine = 7, kWhereTilePrefix = 8, kWhereDispatch = 9,
+  kWhereGemm2 = 6, kWhereCombine = 7, kWhereTilePrefix = 8, kWhereDispatch = 9, kWhereDense = 10,
 };
 
 __device__ __forceinline__ void report(int* status, int code, int where, int detail) {
@@ -158,6 +159,12 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last() {
   return p;
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -228,12 +235,24 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
       "r"(smem_addr(src)), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // every committed store has finished reading its shared-memory source
 __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// all but the most recently committed store have finished reading their source
+__device__ __forceinline__ void bulk_wait_read_all_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 // every committed store has completed
 __device__ __forceinline__ void bulk_wait_all() {
@@ -310,6 +329,46 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cluster_addr) {
       : "memory");
 }
 
+// The same product on 16-bit operands (kind::f16, K = 16, fp32 accumulate; both operands fp16 or
+// both bf16) and on signed 8-bit integers (kind::i8, K = 32, exact int32 accumulate), issued for
+// this CTA or for a pair.
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrives (once) on `bar` when every tcgen05 operation issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
@@ -346,6 +405,31 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
+}
+
+// The same for an MN-major tile of 16-bit elements: the contraction index is the row (128 bytes =
+// 64 elements of the M or N index), 8-row atoms 1024 bytes apart (SBO), and the next 64 elements
+// of M or N `lbo` bytes further.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptors of kind::f16 (D fp32; A and B fp16 = 0 or bf16 = 1 at bits 7 and 10;
+// MN-major operands marked at bits 15 and 16) and of kind::i8 (D int32 = 2, A and B signed = 1).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(bool bf16, int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(bf16) << 7) | (static_cast<uint32_t>(bf16) << 10) |
+         (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // Instruction descriptor of kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (format 0), both
@@ -421,6 +505,21 @@ __device__ __forceinline__ float silu(float g) {
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   return static_cast<uint16_t>(
       __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
+}
+
+// Eight values to signed 8-bit codes rne(v / s) in [-127, 127] (IEEE division; a NaN quotient
+// gives 0), lowest index in the lowest byte.
+__device__ __forceinline__ int int8_code(float v, float s) {
+  return min(127, max(-127, __float2int_rn(__fdiv_rn(v, s))));
+}
+__device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d, float s) {
+  return (static_cast<uint32_t>(int8_code(a, s)) & 0xFFu) |
+         ((static_cast<uint32_t>(int8_code(b, s)) & 0xFFu) << 8) |
+         ((static_cast<uint32_t>(int8_code(c, s)) & 0xFFu) << 16) |
+         (static_cast<uint32_t>(int8_code(d, s)) << 24);
+}
+__device__ __forceinline__ uint2 int8x8(const float (&v)[8], float s) {
+  return make_uint2(int8x4(v[0], v[1], v[2], v[3], s), int8x4(v[4], v[5], v[6], v[7], s));
 }
 
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {

@@ -1,0 +1,69 @@
+// Dense (ungrouped) GEMMs on the 5th-generation tensor cores: internal launch structures (not part
+// of the C ABI). D = A B^T with A [M, K] tokens (or, for a weight gradient, channels) and B [N, K]
+// weights; either operand may instead be stored with its contraction index outermost ("MN-major":
+// A as [K, M], B as [K, N]), so a backward pass needs no transposed copies.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// What the epilogue makes of the accumulators (fp32, or exact int32 for int8 operands).
+constexpr int kEpiStore = 0;      // D rounded once to 16 bits
+constexpr int kEpiGated = 1;      // columns [gate | up]: act(gate) * up, and h itself when kept
+constexpr int kEpiGatedGrad = 2;  // D = dL/d(act(g) u): with h, dL/dg, dL/du and act(g) u
+constexpr int kEpiInt8 = 3;       // row scale x column scale x D (+ bias)
+
+// operand and output types (include/moe_ops.h)
+constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2;
+constexpr int kActSilu = 0, kActGeluTanh = 1;
+
+// One product of a launch. The maps' boxes are chosen by dense_maps for the launch's tile.
+struct DenseProblem {
+  CUtensorMap a, b;
+  CUtensorMap out;               // D (kEpiStore, kEpiInt8), act (the gated ones)
+  CUtensorMap out_h;             // h or dh as [M][2][N] (the gated ones)
+  int M, N, K;                   // valid sizes; gated: N = F (gate and up columns each)
+  int a_mn, b_mn;                // 1: the operand's contraction index is outermost
+  int m_tiles, n_tiles, num_kb;  // set by launch_dense
+  int tile0;                     // first tile of this product in the launch's tile list
+};
+
+constexpr int kMaxProblems = 3;
+struct DenseArgs {
+  DenseProblem p[kMaxProblems];
+  int n_problems, total_tiles;
+  int type, act;                 // 16-bit operands and outputs; int8: the output's type
+  int save_h;                    // kEpiGated: write h
+  const uint16_t* h;             // kEpiGatedGrad: h [M][2][N]
+  const float *row_scale, *col_scale, *bias;   // kEpiInt8 (bias may be null)
+  int* status;
+};
+
+// Tile of a launch: `pair` = 256 x 256 on a 2-CTA pair, else 128 x 128 on one CTA.
+struct DenseTile {
+  bool pair;
+};
+DenseTile dense_tile(int64_t M);
+
+// Tensor maps of one operand. rows x K elements of `bytes` (2 or 1) bytes, K-major unless mn.
+bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
+                       int type, bool mn, bool is_a, bool pair);
+// Gated weights [2][F][K] and output maps [M][N] / [M][2][N].
+bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, bool pair);
+bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type);
+bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type);
+
+cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s);
+
+// Host helpers of moe_api.cu shared by the entry points.
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box,
+              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_UINT8,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+int check_device();
+
+}  // namespace moe

@@ -1,0 +1,649 @@
+// Dense GEMMs on the 5th-generation tensor cores (tcgen05): D = A B^T for the 16-bit gated FFN
+// (forward and backward) and the int8 product with token and channel scales, with their
+// elementwise work fused into the epilogue.
+//
+// Mathematics, per epilogue (dense.cuh):
+//   kEpiGated      h = x W13^T; act = f(h_gate) h_up in fp32 from the unrounded accumulators,
+//                  rounded once; h rounded once when the caller keeps it for the backward pass
+//   kEpiGatedGrad  D = dy W2 = dL/da (never stored); with a = f(g) u:  dL/dg = D u f'(g),
+//                  dL/du = D f(g); dh = [dL/dg | dL/du] and a rounded once to the operands' type
+//   kEpiStore      D rounded once
+//   kEpiInt8       out = s_x[t] s_w[n] D[t, n] (+ bias[n]), D an exact int32 sum
+//
+// Orientation: the MMA's M (TMEM lanes) are the rows of A (tokens), its N the rows of B, so an
+// epilogue thread owns one token's consecutive columns: 16-byte pieces of 128-byte-swizzled rows of
+// shared memory, which leave by TMA tensor stores (clipped at the tensor's edge, so ragged T, d
+// and F need no other path).
+// Operands K-major or MN-major (tcgen05 takes both for 16-bit types), so the backward products
+// dy W2, dh W13, dh^T x and dy^T a read the forward's tensors as they lie.
+//
+// Pipeline: TMA (128-byte swizzle) into a ring of stages of 128 bytes of K, one thread issuing
+// tcgen05.mma into double-buffered TMEM accumulators, four epilogue warps; persistent grid, every
+// wait bounded. Two tiles:
+//   pair    256 x 256 on a 2-CTA pair (cta_group::2, M = 256): each CTA stages 128 rows of A and
+//           128 of B per K-block (32 KB) for 256 x 256 of product, so a byte of shared memory
+//           feeds twice the work of a 128 x 128 tile;
+//   single  128 x 128 on one CTA, for at most 128 rows of A.
+#include <algorithm>
+
+#include "common.cuh"
+#include "dense.cuh"
+#include "kernels.cuh"
+
+namespace moe {
+
+template <int EPI, bool PAIR>
+struct DenseCfg {
+  static constexpr bool I8 = EPI == kEpiInt8;
+  static constexpr int BN = PAIR ? 256 : 128;
+  static constexpr int NB = PAIR ? BN / 2 : BN;      // rows of B staged by one CTA
+  static constexpr int KE = I8 ? 128 : 64;           // elements of K per stage (128 bytes)
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = NB * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  // epilogue staging, per warp: 32 rows x 128 bytes per buffer; the gated epilogues write up to
+  // three tensors per column chunk, the others alternate two buffers
+  static constexpr int BUFS = (EPI == kEpiGated || EPI == kEpiGatedGrad) ? 3 : 2;
+  static constexpr int STG_BYTES = 4 * BUFS * 4096;
+  static constexpr int SMEM_MAX = 232448;
+  static constexpr int STAGES = (SMEM_MAX - 1024 - STG_BYTES - 256) / STAGE_BYTES;
+  static constexpr int SMEM = 1024 + STG_BYTES + STAGES * STAGE_BYTES + 256;
+  static constexpr int TMEM_COLS = 2 * BN;
+  static_assert(STAGES >= 4, "pipeline too shallow");
+};
+
+// sigmoid with the fast exponential and division; the exponent is clamped so that the denominator
+// stays finite (relative error ~1e-6, far below the 16-bit rounding that follows).
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __fdividef(1.f, 1.f + __expf(fminf(-x, 80.f)));
+}
+
+// f(g) = g s with s = sigmoid(g) (SiLU) or sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3) (GELU,
+// tanh form: 0.5 (1 + tanh z) = sigmoid(2 z)); df = s + g s (1 - s) d(argument)/dg.
+template <bool GRAD>
+__device__ __forceinline__ void gate_fn(int act, float g, float& f, float& df) {
+  constexpr float kC = 1.5957691216057308f;          // 2 sqrt(2 / pi)
+  constexpr float kB = 0.044715f;
+  float arg = g, slope = 1.f;
+  if (act == kActGeluTanh) {
+    const float g2 = g * g;
+    arg = kC * g * fmaf(kB, g2, 1.f);
+    if (GRAD) slope = kC * fmaf(3.f * kB, g2, 1.f);
+  }
+  const float s = sigmoid_fast(arg);
+  f = g * s;
+  if (GRAD) df = fmaf(f * (1.f - s), slope, s);
+}
+
+__device__ __forceinline__ uint32_t pack16(int type, float lo, float hi) {
+  if (type == kBf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void unpack16(int type, uint32_t w, float& lo, float& hi) {
+  if (type == kBf16) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xFFFF0000u);
+  } else {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = v.x;
+    hi = v.y;
+  }
+}
+
+// tile -> product p, m-tile, n-tile: inside a product, groups of 8 m-tiles with m fastest, so the
+// units running at one time share both operands' rows in L2.
+__device__ __forceinline__ void dense_tile_at(const DenseArgs& a, int tile, int& p, int& m, int& n) {
+  p = 0;
+  while (p + 1 < a.n_problems && tile >= a.p[p + 1].tile0) ++p;
+  constexpr int GM = 8;
+  const int local = tile - a.p[p].tile0;
+  const int per = GM * a.p[p].n_tiles;
+  const int g = local / per, r = local % per;
+  const int gm = min(GM, a.p[p].m_tiles - g * GM);
+  m = g * GM + r % gm;
+  n = r / gm;
+}
+
+// Writes half (16 words = 32 values of 16 bits) or all of this lane's 128-byte row of a staging
+// buffer: 16-byte piece c of row r sits at piece c ^ (r & 7), the 128-byte swizzle of the store's
+// tensor map (conflict-free for 8 lanes writing the same piece).
+template <int NW>
+__device__ __forceinline__ void stage_row(uint8_t* buf, int lane, int piece0,
+                                          const uint32_t (&w)[NW]) {
+#pragma unroll
+  for (int i = 0; i < NW / 4; ++i)
+    *reinterpret_cast<uint4*>(buf + lane * 128 + (((piece0 + i) ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <int EPI, bool PAIR>
+__global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constant__ DenseArgs args) {
+  pdl_wait();      // predecessor kernel complete, its writes visible
+  pdl_trigger();   // let the next kernel launch
+  using C = DenseCfg<EPI, PAIR>;
+  constexpr int BN = C::BN;
+  constexpr bool kGatedCols = EPI == kEpiGated;     // B tile = BN/2 gate rows + BN/2 up rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* stages = smem;
+  uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::STG_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = PAIR ? cluster_rank() : 0u;
+  const bool leader = crank == 0;
+  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  const int total_tiles = args.total_tiles;
+  if (unit >= total_tiles) return;                  // (both CTAs of a pair together)
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], PAIR ? 8 : 4);
+    }
+    mbar_init(drain, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 2) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before_sync();
+  if constexpr (PAIR) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t full_l = PAIR ? cluster_addr(full, 0) : 0u;
+  const uint32_t tempty_l = PAIR ? cluster_addr(tempty, 0) : 0u;
+
+  auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int stage, int x, int y, uint64_t pol) {
+    if constexpr (PAIR) tma_load_2d_pair(dst, m, full_l + 8u * stage, x, y, pol);
+    else tma_load_2d(dst, m, &full[stage], x, y, pol);
+  };
+  auto load3 = [&](uint8_t* dst, const CUtensorMap* m, int stage, int x, int y, int z,
+                   uint64_t pol) {
+    if constexpr (PAIR) tma_load_3d_pair(dst, m, full_l + 8u * stage, x, y, z, pol);
+    else tma_load_3d(dst, m, &full[stage], x, y, z, pol);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = unit; ok && tile < total_tiles; tile += nunits) {
+        int pi, mt, nt;
+        dense_tile_at(args, tile, pi, mt, nt);
+        const DenseProblem& P = args.p[pi];
+        const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128;
+        const int n0 = nt * BN + static_cast<int>(crank) * C::NB;
+        const int a_mn = P.a_mn, b_mn = P.b_mn, num_kb = P.num_kb;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
+                                : mbar_wait(&empty[stage], phase ^ 1u);
+          if (!got) {
+            report(args.status, kStatusDeviceTimeout, kWhereDense, 1);
+            ok = false;
+            break;
+          }
+          uint8_t* sa = stages + stage * C::STAGE_BYTES;
+          uint8_t* sb = sa + C::A_BYTES;
+          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+          if (!C::I8 && a_mn) {
+            load2(sa, &P.a, stage, m0, kb * 64, pol);
+            load2(sa + 8192, &P.a, stage, m0 + 64, kb * 64, pol);
+          } else {
+            load2(sa, &P.a, stage, kb * C::KE, m0, pol);
+          }
+          if constexpr (kGatedCols) {
+            if constexpr (PAIR) {
+              load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), static_cast<int>(crank), pol);
+            } else {
+              load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), 0, pol);
+              load3(sb + C::B_BYTES / 2, &P.b, stage, kb * C::KE, nt * (BN / 2), 1, pol);
+            }
+          } else if (!C::I8 && b_mn) {
+#pragma unroll
+            for (int i = 0; i < C::NB / 64; ++i)
+              load2(sb + i * 8192, &P.b, stage, n0 + 64 * i, kb * 64, pol);
+          } else {
+            load2(sb, &P.b, stage, kb * C::KE, n0, pol);
+          }
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the most recent load of every stage must land before the CTA exits (the odd CTA of a
+      // pair relies on the final cluster barrier, which the even one reaches after this drain)
+      const int outstanding = leader ? min(issued, C::STAGES) : 0;
+      for (int i = 0; i < outstanding; ++i) {
+        int st = stage - 1 - i;
+        uint32_t ph = phase;
+        while (st < 0) {
+          st += C::STAGES;
+          ph ^= 1u;
+        }
+        mbar_wait(&full[st], ph);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      int stage = 0, t = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t empty_l = PAIR ? cluster_addr(empty, 0) : 0u;
+      const uint32_t empty_p = PAIR ? cluster_addr(empty, 1) : 0u;
+      const uint32_t tfull_l = PAIR ? cluster_addr(tfull, 0) : 0u;
+      const uint32_t tfull_p = PAIR ? cluster_addr(tfull, 1) : 0u;
+      for (int tile = unit; ok && tile < total_tiles; tile += nunits, ++t) {
+        int pi, mt, nt;
+        dense_tile_at(args, tile, pi, mt, nt);
+        const int a_mn = C::I8 ? 0 : args.p[pi].a_mn, b_mn = C::I8 ? 0 : args.p[pi].b_mn;
+        const int num_kb = args.p[pi].num_kb;
+        const uint32_t idesc =
+            C::I8 ? idesc_s8_s32(PAIR ? 256 : 128, BN)
+                  : idesc_f16_f32(args.type == kBf16, PAIR ? 256 : 128, BN, a_mn, b_mn);
+        const int buf = t & 1;
+        const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
+        const bool freed = PAIR ? mbar_wait_cluster(&tempty[buf], tph ^ 1u)
+                                : mbar_wait(&tempty[buf], tph ^ 1u);
+        if (!freed) {
+          report(args.status, kStatusDeviceTimeout, kWhereDense, 2);
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + buf * BN;
+        // descriptor steps of one MMA's K (32 bytes of a row, or 16 rows of 128 bytes), in 16 bytes
+        const uint64_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(&full[stage], phase)) {
+            report(args.status, kStatusDeviceTimeout, kWhereDense, 3);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sa = smem_addr(stages + stage * C::STAGE_BYTES);
+          const uint32_t sb = sa + C::A_BYTES;
+          const uint64_t adesc = a_mn ? smem_desc_sw128_mn(sa, 8192u) : smem_desc_sw128(sa);
+          const uint64_t bdesc = b_mn ? smem_desc_sw128_mn(sb, 8192u) : smem_desc_sw128(sb);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (C::I8)
+              mma_i8<PAIR>(d_tmem, adesc + astep * kk, bdesc + bstep * kk, idesc,
+                           (kb > 0 || kk > 0) ? 1u : 0u);
+            else
+              mma_f16<PAIR>(d_tmem, adesc + astep * kk, bdesc + bstep * kk, idesc,
+                            (kb > 0 || kk > 0) ? 1u : 0u);
+          }
+          if constexpr (PAIR) {
+            mma_commit_pair(empty_l + 8u * stage);
+            mma_commit_pair(empty_p + 8u * stage);
+          } else {
+            mma_commit(&empty[stage]);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) {
+          if constexpr (PAIR) {
+            mma_commit_pair(tfull_l + 8u * buf);
+            mma_commit_pair(tfull_p + 8u * buf);
+          } else {
+            mma_commit(&tfull[buf]);
+          }
+        }
+      }
+      if constexpr (PAIR) mma_commit_pair(cluster_addr(drain, 0));
+      else mma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue (4 warps)
+    const int q = warp & 3;
+    uint8_t* mybuf = staging + q * C::BUFS * 4096;
+    bool bad = false;
+    int t = 0, nb = 0;          // tiles done; staged stores so far (alternating two buffers)
+    for (int tile = unit; tile < total_tiles && !bad; tile += nunits, ++t) {
+      int pi, mt, nt;
+      dense_tile_at(args, tile, pi, mt, nt);
+      const DenseProblem& P = args.p[pi];
+      const int buf = t & 1;
+      const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
+      const int row0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + 32 * q;
+      const int row = row0 + lane;
+      const bool rows_any = row0 < P.M;              // this warp has a valid row
+      float rs = 0.f;
+      if constexpr (EPI == kEpiInt8) rs = row < P.M ? args.row_scale[row] : 0.f;
+      const bool ok = PAIR ? mbar_wait_cluster(&tfull[buf], tph) : mbar_wait(&tfull[buf], tph);
+      bad = __any_sync(0xffffffffu, !ok);
+      if (bad) {
+        if (lane == 0) report(args.status, kStatusDeviceTimeout, kWhereDense, 5);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t tbase = tmem_base + buf * BN + (static_cast<uint32_t>(32 * q) << 16);
+      auto load32 = [&](int c, uint32_t (&r)[32]) {
+        tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+        tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+      };
+      auto store2 = [&](const uint8_t* b, const CUtensorMap* m, int x) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(m, b, x, row0);
+          bulk_commit();
+        }
+      };
+      if (rows_any) {
+        if constexpr (EPI == kEpiStore || EPI == kEpiInt8) {
+          // one 128-byte row of staging per chunk: 64 columns of 16 bits, or 32 of fp32
+          const bool wide = EPI == kEpiInt8 && args.type == kFp32;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            const int col = nt * BN + c;
+            if (col >= P.N) break;
+            uint32_t r[32];
+            load32(c, r);
+            float v[32];
+            if constexpr (EPI == kEpiInt8) {
+              const bool whole = col + 32 <= P.N;    // (N is a multiple of 16)
+              float sc[32];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 s4 = (whole || i < 4)
+                                      ? __ldg(reinterpret_cast<const float4*>(args.col_scale + col) + i)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                sc[4 * i] = s4.x; sc[4 * i + 1] = s4.y; sc[4 * i + 2] = s4.z; sc[4 * i + 3] = s4.w;
+              }
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                v[i] = __int2float_rn(static_cast<int>(r[i])) * (rs * sc[i]);
+              if (args.bias) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (whole || i < 4) {
+                    const float4 b4 = __ldg(reinterpret_cast<const float4*>(args.bias + col) + i);
+                    v[4 * i] += b4.x; v[4 * i + 1] += b4.y; v[4 * i + 2] += b4.z; v[4 * i + 3] += b4.w;
+                  }
+                }
+              }
+            } else {
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            }
+            uint8_t* b = mybuf + (nb & 1) * 4096;
+            const bool first = wide || (c & 32) == 0;
+            if (first) {                             // the store before last has read this buffer
+              if (lane == 0) bulk_wait_read_all_but_one();
+              __syncwarp();
+            }
+            if (wide) {
+              uint32_t w[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+              stage_row(b, lane, 0, w);
+              store2(b, &P.out, col);
+              ++nb;
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = pack16(args.type, v[2 * i], v[2 * i + 1]);
+              stage_row(b, lane, first ? 0 : 4, w);
+              if (!first || col + 32 >= P.N) {
+                store2(b, &P.out, col - (c & 32));
+                ++nb;
+              }
+            }
+          }
+        } else {
+          // Gated epilogues: chunks of 64 features; staging buffer 0 act, 1 gate, 2 up.
+          constexpr int HB = EPI == kEpiGated ? BN / 2 : BN;
+          const bool halves = EPI == kEpiGatedGrad || args.save_h;
+#pragma unroll 1
+          for (int c = 0; c < HB; c += 64) {
+            const int f0 = nt * HB + c;
+            if (f0 >= P.N) break;
+            if (lane == 0) bulk_wait_read_all();     // the previous chunk's stores have read
+            __syncwarp();
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              const int cc = c + 32 * half;
+              uint32_t wa[16], wg[16], wu[16];
+              if constexpr (EPI == kEpiGated) {
+                uint32_t g[32], u[32];
+                load32(cc, g);
+                load32(HB + cc, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float a[2], gf[2], uf[2], unused;
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    gf[e] = __uint_as_float(g[2 * i + e]);
+                    uf[e] = __uint_as_float(u[2 * i + e]);
+                    gate_fn<false>(args.act, gf[e], a[e], unused);
+                    a[e] *= uf[e];
+                  }
+                  wa[i] = pack16(args.type, a[0], a[1]);
+                  wg[i] = pack16(args.type, gf[0], gf[1]);
+                  wu[i] = pack16(args.type, uf[0], uf[1]);
+                }
+              } else {
+                uint4 hg[4], hu[4];
+                const uint16_t* hp = args.h + (size_t)row * 2 * P.N + f0 + 32 * half;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const bool in = row < P.M && f0 + 32 * half + 8 * i < P.N;
+                  hg[i] = in ? __ldg(reinterpret_cast<const uint4*>(hp) + i) : make_uint4(0, 0, 0, 0);
+                  hu[i] = in ? __ldg(reinterpret_cast<const uint4*>(hp + P.N) + i)
+                             : make_uint4(0, 0, 0, 0);
+                }
+                uint32_t da[32];
+                load32(cc, da);
+                tmem_wait_ld();
+                const uint32_t* hgw = reinterpret_cast<const uint32_t*>(hg);
+                const uint32_t* huw = reinterpret_cast<const uint32_t*>(hu);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float g[2], u[2], a[2], dg[2], du[2];
+                  unpack16(args.type, hgw[i], g[0], g[1]);
+                  unpack16(args.type, huw[i], u[0], u[1]);
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    float f, df;
+                    gate_fn<true>(args.act, g[e], f, df);
+                    const float d = __uint_as_float(da[2 * i + e]);
+                    a[e] = f * u[e];
+                    dg[e] = d * u[e] * df;
+                    du[e] = d * f;
+                  }
+                  wa[i] = pack16(args.type, a[0], a[1]);
+                  wg[i] = pack16(args.type, dg[0], dg[1]);
+                  wu[i] = pack16(args.type, du[0], du[1]);
+                }
+              }
+              stage_row(mybuf, lane, 4 * half, wa);
+              if (halves) {
+                stage_row(mybuf + 4096, lane, 4 * half, wg);
+                stage_row(mybuf + 8192, lane, 4 * half, wu);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&P.out, mybuf, f0, row0);
+              if (halves) {
+                tma_store_3d(&P.out_h, mybuf + 4096, f0, 0, row0);
+                tma_store_3d(&P.out_h, mybuf + 8192, f0, 1, row0);
+              }
+              bulk_commit();
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(tempty_l + 8u * buf);
+        else mbar_arrive(&tempty[buf]);
+      }
+    }
+    if (lane == 0) bulk_wait_all();                  // this warp's stores have completed
+  }
+
+  tc_fence_before_sync();
+  if constexpr (PAIR) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 2) {
+    tc_fence_after_sync();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+static CUtensorMapDataType map_type(int type) {
+  return type == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : type == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+}
+
+DenseTile dense_tile(int64_t M) { return DenseTile{M > 128}; }
+
+bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
+                       int type, bool mn, bool is_a, bool pair) {
+  (void)is_a;
+  (void)pair;       // both tiles stage 128 rows of either operand per CTA
+  if (mn) {         // [K][rows]: box 64 elements x 64 of K
+    const uint64_t dims[2] = {(uint64_t)rows, (uint64_t)K};
+    const uint64_t str[1] = {(uint64_t)rows * type_bytes};
+    const uint32_t box[2] = {64, 64};
+    return make_map(m, base, 2, dims, str, box, map_type(type));
+  }
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)K * type_bytes};
+  const uint32_t box[2] = {(uint32_t)(128 / type_bytes), 128};
+  return make_map(m, base, 2, dims, str, box,
+                  type_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(type));
+}
+
+bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, bool pair) {
+  const uint64_t dims[3] = {(uint64_t)K, (uint64_t)F, 2};
+  const uint64_t str[2] = {(uint64_t)K * 2, (uint64_t)F * K * 2};
+  const uint32_t box[3] = {64, pair ? 128u : 64u, 1};
+  return make_map(m, w13, 3, dims, str, box, map_type(type));
+}
+
+bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
+  const int bytes = type == kFp32 ? 4 : 2;
+  const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M};
+  const uint64_t str[1] = {(uint64_t)N * bytes};
+  const uint32_t box[2] = {(uint32_t)(128 / bytes), 32};
+  return make_map(m, base, 2, dims, str, box, map_type(type));
+}
+
+bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type) {
+  const uint64_t dims[3] = {(uint64_t)F, 2, (uint64_t)M};
+  const uint64_t str[2] = {(uint64_t)F * 2, (uint64_t)F * 4};
+  const uint32_t box[3] = {64, 1, 32};
+  return make_map(m, base, 3, dims, str, box, map_type(type));
+}
+
+namespace {
+template <int EPI, bool PAIR>
+cudaError_t launch_dense_t(const DenseArgs& args, cudaStream_t s) {
+  using C = DenseCfg<EPI, PAIR>;
+  static int unit_cache[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!unit_cache[dev]) {
+    err = cudaFuncSetAttribute(dense_gemm_kernel<EPI, PAIR>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (err != cudaSuccess) return err;
+    int units = num_sms();
+    if (PAIR) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(num_sms());
+      cfg.blockDim = dim3(256);
+      cfg.dynamicSmemBytes = C::SMEM;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      err = cudaOccupancyMaxActiveClusters(&clusters, dense_gemm_kernel<EPI, PAIR>, &cfg);
+      if (err != cudaSuccess) return err;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
+      units = std::min(clusters, num_sms() / 2);
+    }
+    unit_cache[dev] = units;
+  }
+  const int units = std::min(unit_cache[dev], args.total_tiles);
+  launch_pdl_cluster(dense_gemm_kernel<EPI, PAIR>, dim3(PAIR ? 2 * units : units), dim3(256),
+                     C::SMEM, PAIR ? 2 : 1, s, args);
+  return cudaGetLastError();
+}
+
+template <int EPI>
+cudaError_t launch_dense_e(DenseTile tile, const DenseArgs& args, cudaStream_t s) {
+  return tile.pair ? launch_dense_t<EPI, true>(args, s) : launch_dense_t<EPI, false>(args, s);
+}
+}  // namespace
+
+cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s) {
+  const int bm = tile.pair ? 256 : 128, bn = tile.pair ? 256 : 128;
+  const int cols = epi == kEpiGated ? bn / 2 : bn;
+  int64_t total = 0;
+  for (int i = 0; i < args.n_problems; ++i) {
+    DenseProblem& p = args.p[i];
+    p.m_tiles = (p.M + bm - 1) / bm;
+    p.n_tiles = (p.N + cols - 1) / cols;
+    p.num_kb = epi == kEpiInt8 ? (p.K + 127) / 128 : (p.K + 63) / 64;
+    p.tile0 = (int)total;
+    total += (int64_t)p.m_tiles * p.n_tiles;
+  }
+  if (total >= (1LL << 30)) return cudaErrorInvalidValue;
+  args.total_tiles = (int)total;
+  switch (epi) {
+    case kEpiStore: return launch_dense_e<kEpiStore>(tile, args, s);
+    case kEpiGated: return launch_dense_e<kEpiGated>(tile, args, s);
+    case kEpiGatedGrad: return launch_dense_e<kEpiGatedGrad>(tile, args, s);
+    case kEpiInt8: return launch_dense_e<kEpiInt8>(tile, args, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,189 @@
+// Entry points of the dense 16-bit gated FFN and its backward pass (include/moe_ops.h): argument
+// checks, tensor maps and the launches of the dense GEMMs (dense_gemm.cu) that do all the work.
+//
+//   forward   1. h = x W13^T, act = f(h_gate) h_up           (one kernel, kEpiGated)
+//             2. y = act W2^T                                 (kEpiStore)
+//   backward  1. dy W2, fused with h: dh and act              (one kernel, kEpiGatedGrad)
+//             2. dW13 = dh^T x, dW2 = dy^T act, dx = dh W13   (one launch, longest products first)
+#include <algorithm>
+
+#include "../../include/moe_ops.h"
+#include "common.cuh"
+#include "dense.cuh"
+#include "kernels.cuh"
+
+namespace moe {
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct FfnPlan {
+  size_t off_act, off_dh, bytes;
+};
+int ffn_plan(const moe_ffn_dims* m, bool backward, FfnPlan* p) {
+  if (!m || m->T < 0 || m->d < 16 || m->d % 16 || m->F < 16 || m->F % 16) return MOE_ERR_INVALID_ARG;
+  if ((m->dtype != MOE_BF16 && m->dtype != MOE_FP16) ||
+      (m->act != MOE_ACT_SILU && m->act != MOE_ACT_GELU_TANH))
+    return MOE_ERR_INVALID_ARG;
+  if (m->T >= (1 << 30) || m->d >= (1 << 28) || m->F >= (1 << 28)) return MOE_ERR_UNSUPPORTED;
+  const size_t rows = (size_t)std::max(m->T, 1);
+  size_t off = 256;                                // status word
+  p->off_act = off;
+  off = align256(off + 2 * rows * m->F);
+  p->off_dh = off;
+  if (backward) off = align256(off + 4 * rows * m->F);
+  p->bytes = off;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_gated_ffn_workspace_bytes(const moe_ffn_dims* dims) {
+  FfnPlan p;
+  return ffn_plan(dims, false, &p) == MOE_OK ? p.bytes : 0;
+}
+
+size_t moe_gated_ffn_backward_workspace_bytes(const moe_ffn_dims* dims) {
+  FfnPlan p;
+  return ffn_plan(dims, true, &p) == MOE_OK ? p.bytes : 0;
+}
+
+int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w13,
+                  const uint16_t* w2, uint16_t* y, uint16_t* h, void* ws, size_t ws_bytes,
+                  void* stream) {
+  FfnPlan p;
+  int rc = ffn_plan(dims, false, &p);
+  if (rc != MOE_OK) return rc;
+  const int T = dims->T, d = dims->d, F = dims->F, type = dims->dtype;
+  if (T == 0) return MOE_OK;
+  if (!x || !w13 || !w2 || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(y, 16) ||
+      (h && !aligned(h, 16)))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < p.bytes || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  rc = check_device();
+  if (rc != MOE_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int* status = reinterpret_cast<int*>(base);
+  uint16_t* act = reinterpret_cast<uint16_t*>(base + p.off_act);
+  if (cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  const DenseTile tile = dense_tile(T);
+  DenseArgs a{};
+  a.n_problems = 1;
+  a.type = type;
+  a.act = dims->act;
+  a.save_h = h != nullptr;
+  a.status = status;
+  DenseProblem& g = a.p[0];
+  g.M = T;
+  g.N = F;
+  g.K = d;
+  if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile.pair) ||
+      !dense_map_gated_weights(&g.b, w13, F, d, type, tile.pair) ||
+      !dense_map_out(&g.out, act, T, F, type) ||
+      !dense_map_out_halves(&g.out_h, h ? h : act, T, h ? F : F / 2, type))
+    return MOE_ERR_UNSUPPORTED;
+  if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  DenseArgs b{};
+  b.n_problems = 1;
+  b.type = type;
+  b.status = status;
+  DenseProblem& o = b.p[0];
+  o.M = T;
+  o.N = d;
+  o.K = F;
+  if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile.pair) ||
+      !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile.pair) ||
+      !dense_map_out(&o.out, y, T, d, type))
+    return MOE_ERR_UNSUPPORTED;
+  return launch_dense(kEpiStore, tile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const uint16_t* x,
+                           const uint16_t* w13, const uint16_t* w2, const uint16_t* h,
+                           uint16_t* dx, uint16_t* dw13, uint16_t* dw2, void* ws, size_t ws_bytes,
+                           void* stream) {
+  FfnPlan p;
+  int rc = ffn_plan(dims, true, &p);
+  if (rc != MOE_OK) return rc;
+  const int T = dims->T, d = dims->d, F = dims->F, type = dims->dtype;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!aligned(dx, 16) || !aligned(dw13, 16) || !aligned(dw2, 16)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) {                                    // sums over no token
+    rc = check_device();
+    if (rc != MOE_OK) return rc;
+    if ((dw13 && cudaMemsetAsync(dw13, 0, 4 * (size_t)F * d, s) != cudaSuccess) ||
+        (dw2 && cudaMemsetAsync(dw2, 0, 2 * (size_t)F * d, s) != cudaSuccess))
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (!dy || !w2 || !h || (dx && !w13) || (dw13 && !x)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(h, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < p.bytes || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  rc = check_device();
+  if (rc != MOE_OK) return rc;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int* status = reinterpret_cast<int*>(base);
+  uint16_t* act = reinterpret_cast<uint16_t*>(base + p.off_act);
+  uint16_t* dh = reinterpret_cast<uint16_t*>(base + p.off_dh);
+  if (cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (!dx && !dw13 && !dw2) return MOE_OK;
+
+  const DenseTile tile = dense_tile(T);
+  DenseArgs a{};
+  a.n_problems = 1;
+  a.type = type;
+  a.act = dims->act;
+  a.h = h;
+  a.status = status;
+  DenseProblem& g = a.p[0];                        // dL/da = dy W2: W2 [d, F] as it lies
+  g.M = T;
+  g.N = F;
+  g.K = d;
+  g.b_mn = 1;
+  if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile.pair) ||
+      !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile.pair) ||
+      !dense_map_out(&g.out, act, T, F, type) || !dense_map_out_halves(&g.out_h, dh, T, F, type))
+    return MOE_ERR_UNSUPPORTED;
+  if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  // The three products that follow are one launch: together they fill the last wave better.
+  struct Product {
+    const void *a, *b;
+    void* out;
+    int M, N, K, a_mn;
+  };
+  const Product all[3] = {{dh, x, dw13, 2 * F, d, T, 1},
+                          {dy, act, dw2, d, F, T, 1},
+                          {dh, w13, dx, T, d, 2 * F, 0}};
+  DenseArgs b{};
+  b.type = type;
+  b.status = status;
+  const DenseTile wtile{true};
+  for (const Product& pr : all) {
+    if (!pr.out) continue;
+    DenseProblem& o = b.p[b.n_problems++];
+    o.M = pr.M;
+    o.N = pr.N;
+    o.K = pr.K;
+    o.a_mn = pr.a_mn;
+    o.b_mn = 1;
+    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, true) ||
+        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, true) ||
+        !dense_map_out(&o.out, pr.out, pr.M, pr.N, type))
+      return MOE_ERR_UNSUPPORTED;
+  }
+  return launch_dense(kEpiStore, wtile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -7,6 +7,7 @@
 
 #include "../../include/moe.h"
 #include "common.cuh"
+#include "dense.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -192,10 +193,9 @@ static EncodeTiledFn encode_fn() {
 
 // 128-byte swizzle, zero fill outside the tensor. dims/strides in elements/bytes, innermost
 // first; strides[i] is the byte stride of dimension i+1.
-static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box,
-                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box, CUtensorMapDataType dtype,
+              CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gd[5], gs[4];
@@ -262,7 +262,7 @@ static bool map_rows(CUtensorMap* m, const uint8_t* a, int64_t rows, int K, int 
 // ---------------------------------------------------------------- helpers
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-static int check_device() {
+int check_device() {
   static int ok_cache[64] = {};   // 0 unknown, 1 ok, 2 bad
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;

@@ -1,4 +1,5 @@
-"""Python binding of the FP8 MoE layer's C ABI (``include/moe.h``), through ctypes.
+"""Python binding of the library's C ABI (``include/moe.h`` and ``include/moe_ops.h``), through
+ctypes.
 
 Argument marshalling only: every step of the layer runs in the CUDA library ``libfp8moe.so``.
 Importing this module loads that library and raises if it has not been built; there is no other
@@ -7,6 +8,7 @@ streams); bf16 tensors are passed as their bit patterns and e4m3 tensors as uint
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -40,6 +42,16 @@ class MoEDebugOut(ctypes.Structure):
                 ("stage_events", ctypes.POINTER(ctypes.c_void_p))]
 
 
+class FFNDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+# moe_dtype and moe_act of include/moe_ops.h
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -54,6 +66,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     dims_p = ctypes.POINTER(MoEDims)
+    ffn_p = ctypes.POINTER(FFNDims)
     sig = {
         "moe_workspace_bytes": (sz, [dims_p]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -70,6 +83,15 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_kernel_launch_count": (ctypes.c_uint64, []),
         "moe_ep_dispatch": (ctypes.c_int, [dims_p, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                            vp, vp, sz, vp]),
+        "moe_quant_int8": (ctypes.c_int, [ctypes.c_int64, i32, i32, vp, vp, vp, vp]),
+        "moe_matmul_int8_workspace_bytes": (sz, [i32, i32, i32]),
+        "moe_matmul_int8": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp,
+                                           vp, sz, vp]),
+        "moe_gated_ffn_workspace_bytes": (sz, [ffn_p]),
+        "moe_gated_ffn_backward_workspace_bytes": (sz, [ffn_p]),
+        "moe_gated_ffn": (ctypes.c_int, [ffn_p, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_gated_ffn_backward": (ctypes.c_int, [ffn_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                                  vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -299,6 +321,142 @@ def moe_forward(hidden, router_w, router_bias, k, k_per_token, w13, w13_scale, w
         _stream(dev), ctypes.byref(dbg_struct) if dbg_struct is not None else None)
     _check(status, "moe_forward")
     return (y, dbg) if debug else y
+
+
+# ------------------------------------------------------------------ int8 and 16-bit operators
+def _on(device: torch.device):
+    """The library launches on the current device: make it the tensors' device for one call."""
+    if device.type != "cuda":
+        raise ValueError("tensor must be on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """Pointer of a contiguous, 16-byte aligned tensor of this dtype, shape and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    p = t.data_ptr()
+    if p & 15:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return p
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, where: str, device) -> torch.Tensor:
+    """The caller's workspace, or one from torch's allocator (reused in stream order)."""
+    if need == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, where)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device:
+        raise ValueError(f"ws must be a uint8 tensor on {device}")
+    return ws
+
+
+def moe_quant_int8(x):
+    """Symmetric int8 quantisation of the rows of x [..., K] (bf16, fp16 or fp32; K a multiple of
+    16): returns (codes int8 [..., K], scale fp32 [...])."""
+    if x.dtype not in DTYPES:
+        raise TypeError("x must be bf16, fp16 or fp32")
+    if x.dim() < 1:
+        raise ValueError("x must have a last dimension")
+    K, dev = x.shape[-1], x.device
+    with _on(dev):
+        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        _check(LIB.moe_quant_int8(scale.numel(), K, DTYPES[x.dtype],
+                                  _arg("x", x, x.dtype, x.shape, dev), codes.data_ptr(),
+                                  scale.data_ptr(), _stream(dev)), "moe_quant_int8")
+    return codes, scale
+
+
+def moe_matmul_int8(x, w, w_scale, bias=None, x_scale=None, out_dtype=None, ws=None):
+    """W8A8 product with a scale per token and output channel: [T, K] x [N, K] -> [T, N].
+
+    x is bf16, fp16 or fp32 (each token is quantised here) or int8 codes with ``x_scale`` fp32 [T];
+    w int8 [N, K]; w_scale fp32 [N]; bias fp32 [N] or None. ``out_dtype`` defaults to x's dtype, or
+    bf16 for codes. K and N are multiples of 16."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [T, K] and w [N, K]")
+    T, K = x.shape
+    N, dev = w.shape[0], x.device
+    codes = x.dtype == torch.int8
+    if not codes and x.dtype not in DTYPES:
+        raise TypeError("x must be bf16, fp16, fp32 or int8 codes")
+    if codes != (x_scale is not None):
+        raise ValueError("x_scale goes with int8 codes, and only with them")
+    out_dtype = out_dtype or (torch.bfloat16 if codes else x.dtype)
+    if out_dtype not in DTYPES:
+        raise TypeError("out_dtype must be bf16, fp16 or fp32")
+    with _on(dev):
+        xp = _arg("x", x, x.dtype, x.shape, dev)
+        wp = _arg("w", w, torch.int8, (N, K), dev)
+        sp = _arg("w_scale", w_scale, torch.float32, (N,), dev)
+        bp = None if bias is None else _arg("bias", bias, torch.float32, (N,), dev)
+        xs = _arg("x_scale", x_scale, torch.float32, (T,), dev) if codes else None
+        ws = _workspace(ws, LIB.moe_matmul_int8_workspace_bytes(T, N, K), "moe_matmul_int8", dev)
+        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+        _check(LIB.moe_matmul_int8(T, N, K, DTYPES.get(x.dtype, 0), None if codes else xp,
+                                   xp if codes else None, xs, wp, sp, bp, DTYPES[out_dtype],
+                                   out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
+               "moe_matmul_int8")
+    return out
+
+
+def _ffn_dims(x, w13, w2, activation) -> FFNDims:
+    if x.dim() != 2 or w13.dim() != 2 or w2.dim() != 2:
+        raise ValueError("x must be [T, d], w13 [2F, d] and w2 [d, F]")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("the gated FFN takes bf16 or fp16")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return FFNDims(x.shape[0], x.shape[1], w2.shape[1], DTYPES[x.dtype], ACTIVATIONS[activation])
+
+
+def moe_gated_ffn(x, w13, w2, activation="silu", save_h=False, ws=None):
+    """y = (act(x Wg^T) * (x Wu^T)) W2^T in bf16 or fp16: x [T, d], w13 [2F, d] (gate rows, then up
+    rows), w2 [d, F]; ``activation`` "silu" or "gelu" (tanh form). Returns y [T, d], and with
+    ``save_h`` also h [T, 2F], the pre-activations that the backward pass takes."""
+    dm = _ffn_dims(x, w13, w2, activation)
+    T, d, F, dev, dt = dm.T, dm.d, dm.F, x.device, x.dtype
+    with _on(dev):
+        xp, w13p = _arg("x", x, dt, (T, d), dev), _arg("w13", w13, dt, (2 * F, d), dev)
+        w2p = _arg("w2", w2, dt, (d, F), dev)
+        ws = _workspace(ws, LIB.moe_gated_ffn_workspace_bytes(ctypes.byref(dm)), "moe_gated_ffn",
+                        dev)
+        y = torch.empty(T, d, dtype=dt, device=dev)
+        h = torch.empty(T, 2 * F, dtype=dt, device=dev) if save_h else None
+        _check(LIB.moe_gated_ffn(ctypes.byref(dm), xp, w13p, w2p, y.data_ptr(),
+                                 h.data_ptr() if save_h else None, ws.data_ptr(), ws.numel(),
+                                 _stream(dev)), "moe_gated_ffn")
+    return (y, h) if save_h else y
+
+
+def moe_gated_ffn_backward(dy, x, w13, w2, h, activation="silu", need=(True, True, True), ws=None):
+    """Gradients (dx [T, d], dw13 [2F, d], dw2 [d, F]) of ``moe_gated_ffn`` for dy [T, d], at the h
+    that the forward call kept. ``need`` says which are wanted; the others come back as None."""
+    dm = _ffn_dims(x, w13, w2, activation)
+    T, d, F, dev, dt = dm.T, dm.d, dm.F, x.device, x.dtype
+    with _on(dev):
+        dyp, xp = _arg("dy", dy, dt, (T, d), dev), _arg("x", x, dt, (T, d), dev)
+        w13p, w2p = _arg("w13", w13, dt, (2 * F, d), dev), _arg("w2", w2, dt, (d, F), dev)
+        hp = _arg("h", h, dt, (T, 2 * F), dev)
+        ws = _workspace(ws, LIB.moe_gated_ffn_backward_workspace_bytes(ctypes.byref(dm)),
+                        "moe_gated_ffn_backward", dev)
+        grads = tuple(torch.empty(n, dtype=dt, device=dev) if want else None
+                      for n, want in zip(((T, d), (2 * F, d), (d, F)), need))
+        gp = [None if g is None else g.data_ptr() for g in grads]
+        _check(LIB.moe_gated_ffn_backward(ctypes.byref(dm), dyp, xp, w13p, w2p, hp, *gp,
+                                          ws.data_ptr(), ws.numel(), _stream(dev)),
+               "moe_gated_ffn_backward")
+    return grads
 
 
 class MoELayerFP8:

@@ -1,0 +1,108 @@
+"""64-bit references and error bounds of the int8 and 16-bit operators (``include/moe_ops.h``).
+
+Every function returns (value in float64, bound): |operator - value| must not exceed the bound, which
+adds up, element by element, what the operator's own arithmetic may be off by:
+
+* a rounding to a type is off by at most U[type] = finfo.eps / 2 of the value (fp16 also by half of its
+  smallest subnormal, 2^-25);
+* a tensor-core sum of K fp32 products by at most K 2^-23 of the sum of magnitudes (each addition may
+  truncate); int8 sums are exact;
+* the fast exponential and division of the activations by a relative 2^-19 (fp32 steps of 2^-21 to
+  2^-23, a handful of them), the tanh form's cubic argument included.
+"""
+from __future__ import annotations
+
+import torch
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -25, torch.float32: 0.0}
+ACC = 2.0 ** -23
+FAST = 2.0 ** -19
+
+
+def quant_int8(x: torch.Tensor):
+    """Codes (float64) and scales (float64): each is an fp32 number by definition, the correctly
+    rounded quotient (a 64-bit quotient of two fp32 numbers rounds to the same fp32 number)."""
+    xd = x.double()
+    amax = xd.abs().amax(dim=-1, keepdim=True)
+    scale = torch.where(amax == 0, torch.ones_like(amax), (amax / 127.0).float().double())
+    codes = torch.round((xd / scale).float().double()).clamp(-127, 127)
+    return codes, scale.squeeze(-1)
+
+
+def matmul_int8(codes, scale, w, w_scale, bias, out_dtype):
+    prod = (codes.double() @ w.double().t()) * scale.double()[:, None] * w_scale.double()[None, :]
+    out = prod if bias is None else prod + bias.double()
+    # int -> fp32, the product of the scales, its product with the sum: 3 fp32 roundings of prod
+    # (a fourth is spare), the bias addition one of out; then the output's rounding
+    near = 4 * U[torch.float32] * prod.abs() + U[torch.float32] * out.abs()
+    return out, near + U[out_dtype] * (out.abs() + near) + TINY[out_dtype]
+
+
+def activation(g, act):
+    """f(g) and f'(g) in float64."""
+    if act == "silu":
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s))
+    a, b = 0.7978845608028654, 0.044715
+    t = torch.tanh(a * (g + b * g ** 3))
+    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * a * (1 + 3 * b * g * g)
+
+
+def _mm(a, b):
+    """a @ b, its magnitude sum |a| @ |b| and the accumulation's bound."""
+    return a @ b, ACC * a.shape[1] * (a.abs() @ b.abs())
+
+
+def gated_ffn(x, w13, w2, act):
+    dt, F = x.dtype, w2.shape[1]
+    u, tiny = U[dt], TINY[dt]
+    x, w13, w2 = x.double(), w13.double(), w2.double()
+    h, eh = _mm(x, w13.t())
+    g, up, eg, eu = h[:, :F], h[:, F:], eh[:, :F], eh[:, F:]
+    f, _ = activation(g, act)
+    a = f * up
+    # |f'| < 1.13 for both activations
+    ea = (1.13 * eg + FAST * f.abs()) * (up.abs() + eu) + f.abs() * eu + FAST * a.abs()
+    ea = ea + u * (a.abs() + ea) + tiny                       # the operand of the second product
+    y, ey = _mm(a, w2.t())
+    ey = ey * (1 + u) + ea @ w2.t().abs()
+    return (y, ey + u * (y.abs() + ey) + tiny), (h, eh + u * (h.abs() + eh) + tiny)
+
+
+def gated_ffn_backward(dy, x, w13, w2, h, act):
+    dt, F = x.dtype, w2.shape[1]
+    u, tiny = U[dt], TINY[dt]
+    dy, x, w13, w2, h = (t.double() for t in (dy, x, w13, w2, h))
+    g, up = h[:, :F], h[:, F:]
+    f, df = activation(g, act)
+    da, eda = _mm(dy, w2)
+    dh = torch.cat([da * up * df, da * f], dim=1)
+    # f' is a sum of terms up to 1 + |g| slope in magnitude, each good to FAST
+    edf = FAST * (2 + g.abs() * (1 if act == "silu" else 4 + g * g))
+    edh = torch.cat([eda * up.abs() * df.abs() + (da.abs() + eda) * up.abs() * edf,
+                     eda * f.abs() + FAST * (da * f).abs()], dim=1)
+    edh = edh + u * (dh.abs() + edh) + tiny
+    a = f * up
+    ea = 2 * FAST * a.abs()
+    ea = ea + u * (a.abs() + ea) + tiny
+
+    def out(p, q, ep, eq):
+        v, ev = _mm(p, q)
+        ev = ev * (1 + u) + (ep @ q.abs() if ep is not None else 0) + (p.abs() @ eq if eq is not None else 0)
+        return v, ev + u * (v.abs() + ev) + tiny
+
+    return (out(dh, w13, edh, None), out(dh.t(), x, edh.t(), None), out(dy.t(), a, None, ea))
+
+
+def check(got: torch.Tensor, ref, what: str, rel: float | None = None):
+    """`got` within the bound everywhere, and in the 2-norm within `rel` of the value."""
+    value, bound = ref
+    assert got.shape == value.shape, what
+    err = (got.double() - value).abs()
+    over = err - bound
+    assert bool((over <= 0).all()), (what, float(err.max()), float(over.max()),
+                                     int((over > 0).sum()), list(value.shape))
+    if rel is not None and value.numel():
+        n = float(torch.linalg.norm(value))
+        assert float(torch.linalg.norm(err)) <= rel * n, (what, float(torch.linalg.norm(err)) / n)
