@@ -13,12 +13,29 @@
 
 namespace moe {
 
+// Scale of a row whose max |value| has these fp32 bits, and four codes: e4m3 (amax / 448; the FP8
+// path's maxima hold no NaN) or int8 (amax / 127; a NaN maximum gives scale NaN and codes 0). Both
+// divisions IEEE fp32; scale 1 for a zero row.
+template <bool I8>
+__device__ __forceinline__ float code_scale(uint32_t amax) {
+  const float am = __uint_as_float(amax);
+  if constexpr (I8) return amax == 0u ? 1.f : __fdiv_rn(am, 127.f);
+  return am > 0.f ? __fdiv_rn(am, 448.f) : 1.f;
+}
+template <bool I8>
+__device__ __forceinline__ uint32_t codes4(float4 v, float sc) {
+  if constexpr (I8) return int8x4(v.x, v.y, v.z, v.w, sc);
+  return static_cast<uint32_t>(e4m3x2(__fdiv_rn(v.x, sc), __fdiv_rn(v.y, sc))) |
+         (static_cast<uint32_t>(e4m3x2(__fdiv_rn(v.z, sc), __fdiv_rn(v.w, sc))) << 16);
+}
+
 // s2[r] = amax[r] / 448 (IEEE fp32; 1 if 0); aq[r, f] = e4m3_rne_satfinite(act[r, f] / s2[r]).
 // The row max is already complete (from the gate/up epilogue), so every 16-element chunk of every
 // row is independent: thread (x, y) of a (chunks x rows) block takes chunk blockIdx.y * blockDim.x
 // + x of rows blockIdx.x * blockDim.y + y, stepping by gridDim.x * blockDim.y (short rows fill the
 // block with several rows); four 16-byte loads in flight per thread and one 16-byte store, no
 // thread divides its index.
+template <bool I8>
 __global__ void __launch_bounds__(256) requant_kernel(const float* __restrict__ act,
                                                       const uint32_t* __restrict__ amax,
                                                       const int32_t* __restrict__ total_rows,
@@ -33,16 +50,14 @@ __global__ void __launch_bounds__(256) requant_kernel(const float* __restrict__ 
   if (c >= n16) return;
 #pragma unroll 2
   for (int r = blockIdx.x * blockDim.y + threadIdx.y; r < R; r += gridDim.x * blockDim.y) {
-    const float am = __uint_as_float(amax[r]);
-    const float sc = am > 0.f ? __fdiv_rn(am, 448.f) : 1.f;
+    const float sc = code_scale<I8>(amax[r]);
     if (c == 0) s2[r] = sc;
     const float4* src = reinterpret_cast<const float4*>(act + (size_t)r * F) + 4 * c;
     const float4 v[4] = {src[0], src[1], src[2], src[3]};
     uint32_t o[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      o[q] = static_cast<uint32_t>(e4m3x2(__fdiv_rn(v[q].x, sc), __fdiv_rn(v[q].y, sc))) |
-             (static_cast<uint32_t>(e4m3x2(__fdiv_rn(v[q].z, sc), __fdiv_rn(v[q].w, sc))) << 16);
+      o[q] = codes4<I8>(v[q], sc);
     reinterpret_cast<uint4*>(aq + (size_t)r * F)[c] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
@@ -51,13 +66,14 @@ __global__ void __launch_bounds__(256) requant_kernel(const float* __restrict__ 
 // (split order fixed), act = silu(gate) * up, s2 = amax|act| / 448 (IEEE fp32; 1 if 0),
 // aq = e4m3(act / s2). One block (up to 1024 threads) per row; act is recomputed in the second
 // pass instead of stored.
+template <bool I8>
 __global__ void __launch_bounds__(1024) swiglu_requant_kernel(
     const float* __restrict__ h, int splits, size_t split_stride,
     const int32_t* __restrict__ total_rows, int64_t rcap, int F, uint8_t* __restrict__ aq,
     float* __restrict__ s2) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
-  __shared__ float red[32];
+  __shared__ uint32_t red[32];
   const int R = (int)min((int64_t)max(*total_rows, 0), rcap);
   const int nv = F / 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
@@ -74,24 +90,26 @@ __global__ void __launch_bounds__(1024) swiglu_requant_kernel(
       }
       return make_float4(silu(g.x) * u.x, silu(g.y) * u.y, silu(g.z) * u.z, silu(g.w) * u.w);
     };
-    float amax = 0.f;
+    uint32_t amax = 0u;                              // max |act| as fp32 bits
     for (int i = threadIdx.x; i < nv; i += blockDim.x) {
       const float4 a = act4(i);
-      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
+      if constexpr (I8)                              // (a NaN counts as the largest)
+        amax = max(max(amax, max(__float_as_uint(fabsf(a.x)), __float_as_uint(fabsf(a.y)))),
+                   max(__float_as_uint(fabsf(a.z)), __float_as_uint(fabsf(a.w))));
+      else                                           // (fmaxf drops it)
+        amax = __float_as_uint(fmaxf(fmaxf(__uint_as_float(amax), fmaxf(fabsf(a.x), fabsf(a.y))),
+                                     fmaxf(fabsf(a.z), fabsf(a.w))));
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    amax = __reduce_max_sync(0xffffffffu, amax);
     if (lane == 0) red[warp] = amax;
     __syncthreads();
-    float am = red[0];
-    for (int w = 1; w < nwarps; ++w) am = fmaxf(am, red[w]);
-    const float sc = am > 0.f ? __fdiv_rn(am, 448.f) : 1.f;
+    uint32_t am = red[0];
+    for (int w = 1; w < nwarps; ++w) am = max(am, red[w]);
+    const float sc = code_scale<I8>(am);
     if (threadIdx.x == 0) s2[r] = sc;
     uint32_t* dst = reinterpret_cast<uint32_t*>(aq + (size_t)r * F);
     for (int i = threadIdx.x; i < nv; i += blockDim.x) {
-      const float4 v = act4(i);
-      dst[i] = static_cast<uint32_t>(e4m3x2(__fdiv_rn(v.x, sc), __fdiv_rn(v.y, sc))) |
-               (static_cast<uint32_t>(e4m3x2(__fdiv_rn(v.z, sc), __fdiv_rn(v.w, sc))) << 16);
+      dst[i] = codes4<I8>(act4(i), sc);
     }
     __syncthreads();                                   // red[] is reused by the next row
   }
@@ -206,7 +224,7 @@ cudaError_t launch_requant(const Plan& p, const float* act, const uint32_t* amax
   const int64_t row_blocks = (p.Rcap + by - 1) / by;
   const int gx = (int)std::min<int64_t>(std::max<int64_t>(row_blocks, 1),
                                         std::max<int64_t>(16LL * num_sms() / gy, 1));
-  launch_pdl(requant_kernel, dim3(gx, gy), dim3(bx, by), 0, s, act, amax, total_rows, p.Rcap,
+  launch_pdl(p.int8 ? requant_kernel<true> : requant_kernel<false>, dim3(gx, gy), dim3(bx, by), 0, s, act, amax, total_rows, p.Rcap,
              p.F, aq, s2);
   return cudaGetLastError();
 }
@@ -216,7 +234,7 @@ cudaError_t launch_swiglu_requant(const Plan& p, const float* h, int splits, siz
                                   cudaStream_t s) {
   // few long rows at decode: up to 1024 threads per row (one float4 of F per thread)
   const int threads = std::min(1024, std::max(128, ((p.F / 4 + 31) / 32) * 32));
-  launch_pdl(swiglu_requant_kernel, dim3(row_grid(p.Rcap)), dim3(threads), 0, s, h, splits,
+  launch_pdl(p.int8 ? swiglu_requant_kernel<true> : swiglu_requant_kernel<false>, dim3(row_grid(p.Rcap)), dim3(threads), 0, s, h, splits,
              split_stride, total_rows, p.Rcap, p.F, aq, s2);
   return cudaGetLastError();
 }

@@ -4,6 +4,7 @@
 //
 //   gate/up GEMM: h = x_scale[r] * w13_scale[e, j] * sum_d xq[r, d] w13[e, j, d];
 //                 epilogue act = silu(h_gate) * h_up, stored fp32, per-row max |act| (atomicMax)
+//   (with int8 codes instead of e4m3, kind::i8 and exact int32 accumulators: template flag I8)
 //   down GEMM:    o = s2[r] * w2_scale[e, i] * sum_f aq[r, f] w2[e, i, f]  (optionally split K)
 //
 // Method: the megakernel page (seventnews.com), W8A8 paragraph and section "Comment fonctionne le
@@ -143,6 +144,20 @@ __device__ __forceinline__ void decode_tile(const TileTable& tt, int tile, int& 
   m = rest / tt.splits;
 }
 
+// An accumulator's value: fp32, or the exact int32 sum of int8 products.
+template <bool I8>
+__device__ __forceinline__ float acc_value(uint32_t r) {
+  return I8 ? __int2float_rn(static_cast<int>(r)) : __uint_as_float(r);
+}
+
+// Running max of |v| as fp32 bits (which order like the values). The FP8 path drops a NaN; the int8
+// path keeps it (NaN bits are above infinity's), so that the row's scale shows it.
+template <bool I8>
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m, float v) {
+  if constexpr (I8) return max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+  return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(v)));
+}
+
 // Valid token rows of the tile starting at row0 of group g, rounded up to a multiple of ROUND.
 template <int BN, int ROUND>
 __device__ __forceinline__ int tile_rows_rounded(const TileTable& tt, int g, int row0) {
@@ -151,7 +166,7 @@ __device__ __forceinline__ int tile_rows_rounded(const TileTable& tt, int g, int
 }
 
 
-template <int BN, int MODE, bool PAIR, int SLABS>
+template <int BN, int MODE, bool PAIR, int SLABS, bool I8>
 __global__ void __launch_bounds__(256, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                         const __grid_constant__ CUtensorMap map_a_shared,
@@ -341,7 +356,8 @@ __global__ void __launch_bounds__(256, 1)
         // MMA N = the tile's valid rows rounded up (M = 128 takes N = 16 .. 256 by 16; the pair's
         // M = 256 the same, here by 32 so that each CTA's half is whole 16-row boxes)
         const int ncols = tile_rows_rounded<BN, C::ROUND>(tt, g, tt.off[g] + n * BN);
-        const uint32_t idesc = idesc_e4m3_f32(PAIR ? 256 : 128, ncols);
+        const uint32_t idesc = I8 ? idesc_s8_s32(PAIR ? 256 : 128, ncols)
+                                  : idesc_e4m3_f32(PAIR ? 256 : 128, ncols);
         int h[2];
         uint32_t ph[2], col[SLABS];
         const int nh = seq.take(ncols, h, ph, col);
@@ -375,8 +391,11 @@ __global__ void __launch_bounds__(256, 1)
             const uint64_t adesc = smem_desc_sw128(sa + j * C::SLAB_BYTES);
             const uint32_t d_tmem = tmem_base + col[j];
 #pragma unroll
-            for (int kk = 0; kk < kBK / 32; ++kk) {  // K = 32 e4m3 (32 bytes) per instruction
-              if constexpr (PAIR)
+            for (int kk = 0; kk < kBK / 32; ++kk) {  // K = 32 codes (32 bytes) per instruction
+              if constexpr (I8)
+                mma_i8<PAIR>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc,
+                             (kb > kb0 || kk > 0) ? 1u : 0u);
+              else if constexpr (PAIR)
                 mma_e4m3_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc,
                               (kb > kb0 || kk > 0) ? 1u : 0u);
               else
@@ -491,27 +510,27 @@ __global__ void __launch_bounds__(256, 1)
               tmem_wait_ld();
               float* xr = xchg + (32 * q + lane) * C::XCHG_LD;
 #pragma unroll
-              for (int c = 0; c < CW; ++c) xr[c] = __uint_as_float(r[c]) * wsv;
+              for (int c = 0; c < CW; ++c) xr[c] = acc_value<I8>(r[c]) * wsv;
             }
             named_bar_sync(1, 128);
             const int nn = c0 + lane;
             if (!bad && lane < CW && nn < nvalid && f0 < args.M_valid) {
               const float rsc = rsv;
               float act[16];
-              float amax = 0.f;
+              uint32_t amax = 0u;
 #pragma unroll
               for (int k2 = 0; k2 < 16; ++k2) {
                 const int jf = 16 * q + k2;
                 const float gv = xchg[jf * C::XCHG_LD + lane] * rsc;
                 const float uv = xchg[(64 + jf) * C::XCHG_LD + lane] * rsc;
                 act[k2] = silu(gv) * uv;
-                amax = fmaxf(amax, fabsf(act[k2]));
+                amax = amax_bits<I8>(amax, act[k2]);
               }
               float4* dst = reinterpret_cast<float4*>(args.out + (size_t)(row0 + nn) * args.out_ld + f0);
 #pragma unroll
               for (int v = 0; v < 4; ++v)
                 dst[v] = make_float4(act[4 * v], act[4 * v + 1], act[4 * v + 2], act[4 * v + 3]);
-              atomicMax(&args.row_amax[row0 + nn], __float_as_uint(amax));
+              atomicMax(&args.row_amax[row0 + nn], amax);
             }
             named_bar_sync(1, 128);
           }
@@ -540,7 +559,7 @@ __global__ void __launch_bounds__(256, 1)
             float v[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c)
-              v[c] = __uint_as_float(r[c]) * __shfl_sync(0xffffffffu, rsv, c) * wsv;
+              v[c] = acc_value<I8>(r[c]) * __shfl_sync(0xffffffffu, rsv, c) * wsv;
             if constexpr (C::DOWN_T) {
               // Through this warp's dense 32 x 32 fp32 block of shared memory (row = token): a
               // full chunk leaves by one TMA tensor store, a ragged one by 16-byte stores of its
@@ -612,7 +631,7 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 namespace {
-template <int BN, int MODE, bool PAIR, int SLABS = 1>
+template <int BN, int MODE, bool PAIR, int SLABS = 1, bool I8 = false>
 cudaError_t launch_gemm_t(const CUtensorMap& a, const CUtensorMap& ash, const CUtensorMap& b64,
                           const CUtensorMap& b16, const CUtensorMap& out, const GemmArgs& args,
                           cudaStream_t s) {
@@ -623,7 +642,7 @@ cudaError_t launch_gemm_t(const CUtensorMap& a, const CUtensorMap& ash, const CU
   if (err != cudaSuccess) return err;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!grid_cache[dev]) {
-    err = cudaFuncSetAttribute(grouped_gemm_kernel<BN, MODE, PAIR, SLABS>,
+    err = cudaFuncSetAttribute(grouped_gemm_kernel<BN, MODE, PAIR, SLABS, I8>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     int grid = num_sms();
@@ -641,23 +660,23 @@ cudaError_t launch_gemm_t(const CUtensorMap& a, const CUtensorMap& ash, const CU
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int clusters = 0;
-      err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_kernel<BN, MODE, PAIR, SLABS>, &cfg);
+      err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_kernel<BN, MODE, PAIR, SLABS, I8>, &cfg);
       if (err != cudaSuccess) return err;
       if (clusters < 1) return cudaErrorInvalidConfiguration;
       grid = 2 * std::min(clusters, num_sms() / 2);
     }
     grid_cache[dev] = grid;
   }
-  launch_pdl_cluster(grouped_gemm_kernel<BN, MODE, PAIR, SLABS>, dim3(grid_cache[dev]), dim3(256), C::SMEM,
+  launch_pdl_cluster(grouped_gemm_kernel<BN, MODE, PAIR, SLABS, I8>, dim3(grid_cache[dev]), dim3(256), C::SMEM,
                      PAIR ? 2 : 1, s, a, ash, b64, b16, out, args);
   return cudaGetLastError();
 }
 
-template <int MODE>
+template <int MODE, bool I8>
 cudaError_t launch_by_bn(int BN, bool pair, int slabs, const CUtensorMap& a, const CUtensorMap& ash,
                          const CUtensorMap& b64, const CUtensorMap& b16, const CUtensorMap& out,
                          const GemmArgs& args, cudaStream_t s) {
-  if constexpr (MODE == kModeSwiGLU) {
+  if constexpr (MODE == kModeSwiGLU && !I8) {
     if (pair && slabs == 2) {
       switch (BN) {
         case 128: return launch_gemm_t<128, MODE, true, 2>(a, ash, b64, b16, out, args, s);
@@ -668,24 +687,24 @@ cudaError_t launch_by_bn(int BN, bool pair, int slabs, const CUtensorMap& a, con
     }
   }
   switch (BN) {
-    case 16: return launch_gemm_t<16, MODE, false>(a, ash, b64, b16, out, args, s);
-    case 32: return launch_gemm_t<32, MODE, false>(a, ash, b64, b16, out, args, s);
-    case 64: return launch_gemm_t<64, MODE, false>(a, ash, b64, b16, out, args, s);
+    case 16: return launch_gemm_t<16, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
+    case 32: return launch_gemm_t<32, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
+    case 64: return launch_gemm_t<64, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
     default:
       if constexpr (MODE == kModeGateUpPartial) return cudaErrorInvalidValue;  // decode tiles only
       else {
         if (pair) {
           switch (BN) {
-            case 128: return launch_gemm_t<128, MODE, true>(a, ash, b64, b16, out, args, s);
-            case 192: return launch_gemm_t<192, MODE, true>(a, ash, b64, b16, out, args, s);
-            case 256: return launch_gemm_t<256, MODE, true>(a, ash, b64, b16, out, args, s);
+            case 128: return launch_gemm_t<128, MODE, true, 1, I8>(a, ash, b64, b16, out, args, s);
+            case 192: return launch_gemm_t<192, MODE, true, 1, I8>(a, ash, b64, b16, out, args, s);
+            case 256: return launch_gemm_t<256, MODE, true, 1, I8>(a, ash, b64, b16, out, args, s);
             default: return cudaErrorInvalidValue;
           }
         }
         switch (BN) {
-          case 128: return launch_gemm_t<128, MODE, false>(a, ash, b64, b16, out, args, s);
-          case 192: return launch_gemm_t<192, MODE, false>(a, ash, b64, b16, out, args, s);
-          case 256: return launch_gemm_t<256, MODE, false>(a, ash, b64, b16, out, args, s);
+          case 128: return launch_gemm_t<128, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
+          case 192: return launch_gemm_t<192, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
+          case 256: return launch_gemm_t<256, MODE, false, 1, I8>(a, ash, b64, b16, out, args, s);
           default: return cudaErrorInvalidValue;
         }
       }
@@ -693,19 +712,30 @@ cudaError_t launch_by_bn(int BN, bool pair, int slabs, const CUtensorMap& a, con
 }
 }  // namespace
 
+namespace {
+template <bool I8>
+cudaError_t gateup(const Plan& p, const CUtensorMap& w13, const CUtensorMap& w13s,
+                   const CUtensorMap& acts64, const CUtensorMap& acts16, const GemmArgs& a,
+                   bool partial, cudaStream_t s) {
+  // (the output map is used by the down GEMM only; the weight map stands in)
+  if (partial)
+    return launch_by_bn<kModeGateUpPartial, I8>(p.BN, false, 1, w13, w13s, acts64, acts16, w13, a, s);
+  return launch_by_bn<kModeSwiGLU, I8>(p.BN, p.pair1, p.slabs1, w13, w13s, acts64, acts16, w13, a, s);
+}
+}  // namespace
+
 cudaError_t launch_gemm_gateup(const Plan& p, const CUtensorMap& w13, const CUtensorMap& w13s,
                                const CUtensorMap& acts64, const CUtensorMap& acts16,
                                const GemmArgs& a, bool partial, cudaStream_t s) {
-  // (the output map is used by the down GEMM only; the weight map stands in)
-  if (partial)
-    return launch_by_bn<kModeGateUpPartial>(p.BN, false, 1, w13, w13s, acts64, acts16, w13, a, s);
-  return launch_by_bn<kModeSwiGLU>(p.BN, p.pair1, p.slabs1, w13, w13s, acts64, acts16, w13, a, s);
+  return p.int8 ? gateup<true>(p, w13, w13s, acts64, acts16, a, partial, s)
+                : gateup<false>(p, w13, w13s, acts64, acts16, a, partial, s);
 }
 
 cudaError_t launch_gemm_down(const Plan& p, const CUtensorMap& w2, const CUtensorMap& w2s,
                              const CUtensorMap& acts64, const CUtensorMap& acts16,
                              const CUtensorMap& out, const GemmArgs& a, cudaStream_t s) {
-  return launch_by_bn<kModeDown>(p.BN, p.pair2, 1, w2, w2s, acts64, acts16, out, a, s);
+  return p.int8 ? launch_by_bn<kModeDown, true>(p.BN, p.pair2, 1, w2, w2s, acts64, acts16, out, a, s)
+                : launch_by_bn<kModeDown, false>(p.BN, p.pair2, 1, w2, w2s, acts64, acts16, out, a, s);
 }
 
 }  // namespace moe

@@ -24,6 +24,7 @@ struct Plan {
   int64_t Rpad;      // rows allocated for row-indexed buffers (>= Rcap, >= 256)
   int BN;            // token tile of the grouped GEMMs (max MMA N; a tile uses its valid rows)
   bool pair1, pair2; // gate/up, down GEMM on 2-CTA pairs (M = 256 tcgen05 MMA)
+  bool int8;         // codes are signed 8-bit integers instead of e4m3
   int slabs1;        // weight slabs of 128 rows per CTA in the gate/up GEMM (2: pairs only)
   int r_splits, r_chunks_per_split;           // router: split of d into 32-wide chunks
   int g1_kb, g1_m_tiles;                      // gate/up GEMM: K blocks (d/128), 64-row tiles
@@ -183,6 +184,10 @@ cudaError_t launch_ep_dispatch(const Plan& p, int n_ranks, const uint16_t* hidde
                                const int32_t* k_per_token, uint16_t* send_hidden,
                                int32_t* send_ids, float* send_w, int32_t* send_counts,
                                int32_t* slot_of, float* slot_w, int* status, cudaStream_t s);
+
+// int8 codes and scales of each row (int8.cu); clears the 16-byte status word when one is given.
+cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8_t* codes,
+                              float* scale, int* status, cudaStream_t s);
 
 int num_sms();
 

@@ -5,7 +5,7 @@
 #include <algorithm>
 #include <cstring>
 
-#include "../../include/moe.h"
+#include "../../include/moe_ops.h"
 #include "common.cuh"
 #include "dense.cuh"
 #include "kernels.cuh"
@@ -445,6 +445,51 @@ static int run_ffn(const Plan& p, const Ws& w, const uint8_t* w13, const float* 
   return MOE_OK;
 }
 
+// moe_grouped_ffn_fp8 and moe_grouped_ffn_int8: the same steps on codes of either format.
+static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, const uint8_t* w13,
+                       const float* w13_scale, const uint8_t* w2, const float* w2_scale,
+                       const int32_t* expert_offsets, const int32_t* perm_token, float* expert_out,
+                       float* act_scale_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!dims) return MOE_ERR_INVALID_ARG;
+  Plan p;
+  MOE_TRY(plan_make(dims->T, dims->d, dims->E, dims->F, dims->k_max, dims->F_shared, &p));
+  if (p.T == 0) return MOE_OK;
+  if (!hidden || !w13 || !w13_scale || !w2 || !w2_scale || !expert_offsets || !perm_token ||
+      !expert_out)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(expert_out, 16))
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(p, ws, ws_bytes));
+  MOE_TRY(check_device());
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Ws w = carve(p, ws);
+  Plan q = p;
+  q.shared = false;
+  q.G = p.E;
+  q.Rcap = (int64_t)p.T * p.k_max;
+  q.int8 = int8;
+  if (int8)
+    MOE_CUDA(launch_quant_int8(p.T, p.d, kBf16, hidden, reinterpret_cast<int8_t*>(w.xq), w.xs,
+                               nullptr, s));
+  else
+    MOE_CUDA(launch_topk_quant(q, nullptr, nullptr, 1, nullptr, nullptr, nullptr, hidden, w.xq,
+                               w.xs, false, true, nullptr, w.status, s));
+  if (act_scale_out)
+    MOE_CUDA(cudaMemcpyAsync(act_scale_out, w.xs, sizeof(float) * p.T, cudaMemcpyDeviceToDevice, s));
+  MOE_CUDA(launch_tile_prefix(q, expert_offsets, w.tiles, w.status, s));
+  // the grouped FFN reads offsets/perm from the workspace copies: keep one layout for both paths
+  MOE_CUDA(cudaMemcpyAsync(w.offsets, expert_offsets, sizeof(int32_t) * (p.E + 1),
+                           cudaMemcpyDeviceToDevice, s));
+  MOE_CUDA(cudaMemcpyAsync(w.perm, perm_token, sizeof(int32_t) * q.Rcap, cudaMemcpyDeviceToDevice, s));
+  const bool direct = p.g2_splits == 1;
+  MOE_TRY(run_ffn(q, w, w13, w13_scale, w2, w2_scale, nullptr, nullptr, nullptr, nullptr,
+                  direct ? expert_out : w.o, (size_t)p.Rpad * p.d, q.Rcap, nullptr, s));
+  if (!direct)
+    MOE_CUDA(launch_reduce_splits(q, w.o, p.g2_splits, (size_t)p.Rpad * p.d, w.offsets + p.E,
+                                  expert_out, s));
+  return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -559,39 +604,20 @@ int moe_grouped_ffn_fp8(const moe_dims* dims, const uint16_t* hidden, const uint
                         const int32_t* expert_offsets, const int32_t* perm_token,
                         float* expert_out, float* act_scale_out, void* ws, size_t ws_bytes,
                         void* stream) {
-  if (!dims) return MOE_ERR_INVALID_ARG;
-  Plan p;
-  MOE_TRY(plan_make(dims->T, dims->d, dims->E, dims->F, dims->k_max, dims->F_shared, &p));
-  if (p.T == 0) return MOE_OK;
-  if (!hidden || !w13 || !w13_scale || !w2 || !w2_scale || !expert_offsets || !perm_token ||
-      !expert_out)
-    return MOE_ERR_INVALID_ARG;
-  if (!aligned(hidden, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(expert_out, 16))
-    return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(p, ws, ws_bytes));
-  MOE_TRY(check_device());
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Ws w = carve(p, ws);
-  Plan q = p;
-  q.shared = false;
-  q.G = p.E;
-  q.Rcap = (int64_t)p.T * p.k_max;
-  MOE_CUDA(launch_topk_quant(q, nullptr, nullptr, 1, nullptr, nullptr, nullptr, hidden, w.xq,
-                             w.xs, false, true, nullptr, w.status, s));
-  if (act_scale_out)
-    MOE_CUDA(cudaMemcpyAsync(act_scale_out, w.xs, sizeof(float) * p.T, cudaMemcpyDeviceToDevice, s));
-  MOE_CUDA(launch_tile_prefix(q, expert_offsets, w.tiles, w.status, s));
-  // the grouped FFN reads offsets/perm from the workspace copies: keep one layout for both paths
-  MOE_CUDA(cudaMemcpyAsync(w.offsets, expert_offsets, sizeof(int32_t) * (p.E + 1),
-                           cudaMemcpyDeviceToDevice, s));
-  MOE_CUDA(cudaMemcpyAsync(w.perm, perm_token, sizeof(int32_t) * q.Rcap, cudaMemcpyDeviceToDevice, s));
-  const bool direct = p.g2_splits == 1;
-  MOE_TRY(run_ffn(q, w, w13, w13_scale, w2, w2_scale, nullptr, nullptr, nullptr, nullptr,
-                  direct ? expert_out : w.o, (size_t)p.Rpad * p.d, q.Rcap, nullptr, s));
-  if (!direct)
-    MOE_CUDA(launch_reduce_splits(q, w.o, p.g2_splits, (size_t)p.Rpad * p.d, w.offsets + p.E,
-                                  expert_out, s));
-  return MOE_OK;
+  return grouped_ffn(false, dims, hidden, w13, w13_scale, w2, w2_scale, expert_offsets, perm_token,
+                     expert_out, act_scale_out, ws, ws_bytes, stream);
+}
+
+int moe_grouped_ffn_int8(const moe_dims* dims, const uint16_t* hidden, const int8_t* w13,
+                         const float* w13_scale, const int8_t* w2, const float* w2_scale,
+                         const int32_t* expert_offsets, const int32_t* perm_token,
+                         float* expert_out, float* act_scale_out, void* ws, size_t ws_bytes,
+                         void* stream) {
+  // int32 sums over d and F stay exact for any codes: 128 * 128 * 131056 < 2^31
+  if (dims && (dims->d > 131056 || dims->F > 131056)) return MOE_ERR_UNSUPPORTED;
+  return grouped_ffn(true, dims, hidden, reinterpret_cast<const uint8_t*>(w13), w13_scale,
+                     reinterpret_cast<const uint8_t*>(w2), w2_scale, expert_offsets, perm_token,
+                     expert_out, act_scale_out, ws, ws_bytes, stream);
 }
 
 int moe_combine(const moe_dims* dims, const float* expert_out, const float* topk_w,

@@ -87,6 +87,8 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_matmul_int8_workspace_bytes": (sz, [i32, i32, i32]),
         "moe_matmul_int8": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp,
                                            vp, sz, vp]),
+        "moe_grouped_ffn_int8": (ctypes.c_int, [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                sz, vp]),
         "moe_gated_ffn_workspace_bytes": (sz, [ffn_p]),
         "moe_gated_ffn_backward_workspace_bytes": (sz, [ffn_p]),
         "moe_gated_ffn": (ctypes.c_int, [ffn_p, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -229,6 +231,36 @@ def moe_grouped_ffn_fp8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets, pe
                                    _p(w13_scale), _p(_u8(w2)), _p(w2_scale), _p(expert_offsets),
                                    _p(perm_token), _p(out), _p(xs), _p(ws), ws.numel(),
                                    _stream(dev)), "moe_grouped_ffn_fp8")
+    return (out, xs) if want_act_scale else out
+
+
+def moe_grouped_ffn_int8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets, perm_token, k_max,
+                         ws=None, want_act_scale=False):
+    """Grouped W8A8 int8 SwiGLU experts over routed rows: ``moe_grouped_ffn_fp8`` with int8 codes
+    (w13 [E, 2F, d], w2 [E, d, F], scales as there). Returns expert_out fp32 [T*k_max, d] (rows
+    behind the last routed one are zero), and the per-token activation scales when asked."""
+    if hidden.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("hidden must be [T, d], w13 [E, 2F, d] and w2 [E, d, F]")
+    T, d = hidden.shape
+    E, F, dev = w13.shape[0], w2.shape[2], hidden.device
+    dm = dims(T, d, E, F, k_max)
+    with _on(dev):
+        args = [_arg("hidden", hidden, torch.bfloat16, (T, d), dev),
+                _arg("w13", w13, torch.int8, (E, 2 * F, d), dev),
+                _arg("w13_scale", w13_scale, torch.float32, (E, 2 * F), dev),
+                _arg("w2", w2, torch.int8, (E, d, F), dev),
+                _arg("w2_scale", w2_scale, torch.float32, (E, d), dev),
+                _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev)]
+        if perm_token.dtype != torch.int32 or perm_token.device != dev:
+            raise TypeError(f"perm_token must be int32 on {dev}")
+        if perm_token.numel() < T * k_max or not perm_token.is_contiguous():
+            raise ValueError("perm_token must be contiguous and hold T * k_max rows")
+        ws = alloc_workspace(dm, dev) if ws is None else ws
+        out = torch.zeros(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
+        xs = torch.empty(T, dtype=torch.float32, device=dev) if want_act_scale else None
+        _check(LIB.moe_grouped_ffn_int8(ctypes.byref(dm), *args, perm_token.data_ptr(),
+                                        out.data_ptr(), _p(xs), _p(ws), ws.numel(),
+                                        _stream(dev)), "moe_grouped_ffn_int8")
     return (out, xs) if want_act_scale else out
 
 

@@ -7,7 +7,7 @@
  * The conventions of moe.h hold: device pointers, dense row-major tensors, 16-byte alignment where
  * noted, a caller-owned workspace of the size asked for (256-byte aligned), asynchronous calls on
  * `stream`, negative moe_status values for what the host can check. Every entry point with a
- * workspace clears its status word first; moe_device_status(ws, ...) reads it after the call.
+ * workspace clears its status word first (moe_grouped_ffn_int8 excepted); moe_device_status(ws, ...) reads it after the call.
  * Calls whose workspaces differ are independent; two calls that may overlap need two workspaces.
  */
 #ifndef FP8_MOE_OPS_H
@@ -50,6 +50,20 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
                     const int8_t* codes, const float* x_scale, const int8_t* w,
                     const float* w_scale, const float* bias, int32_t out_type, void* out, void* ws,
                     size_t ws_bytes, void* stream);
+
+/* The routed experts in int8: moe_grouped_ffn_fp8 (moe.h) with int8 codes in place of e4m3. For every
+ * routed row r of expert e with token t = perm_token[r], both scales and codes by moe_quant_int8's rule:
+ *   s_t, xq = quantised hidden[t,:];   h[j] = s_t * w13_scale[e,j] * sum_d xq[d] * w13[e,j,d];
+ *   act[f] = silu(h[f]) * h[F+f] (fp32);  s2, aq = quantised act over all F;
+ *   expert_out[r,i] = s2 * w2_scale[e,i] * sum_f aq[f] * w2[e,i,f]
+ *   w13 [E, 2F, d] int8; w2 [E, d, F] int8; every other argument, the layouts, the workspace
+ *   (moe_workspace_bytes) and the errors as for moe_grouped_ffn_fp8; like it, this entry point leaves
+ *   the status word as it is. d and F at most 131056. */
+int moe_grouped_ffn_int8(const moe_dims* dims, const uint16_t* hidden, const int8_t* w13,
+                         const float* w13_scale, const int8_t* w2, const float* w2_scale,
+                         const int32_t* expert_offsets, const int32_t* perm_token,
+                         float* expert_out, float* act_scale_out, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* Sizes of a dense gated FFN: T tokens, hidden size d, width F (multiples of 16); dtype MOE_BF16 or
  * MOE_FP16 (operands, gradients and outputs); act a moe_act. */

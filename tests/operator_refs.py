@@ -106,3 +106,49 @@ def check(got: torch.Tensor, ref, what: str, rel: float | None = None):
     if rel is not None and value.numel():
         n = float(torch.linalg.norm(value))
         assert float(torch.linalg.norm(err)) <= rel * n, (what, float(torch.linalg.norm(err)) / n)
+
+
+def _block_sums(p, q):
+    """sum_b |p_b q_b^T| over blocks of 128 of the contraction. A split contraction adds fp32 partial
+    sums P_s, each over whole blocks, so sum_s |P_s| <= this (triangle inequality)."""
+    out = torch.zeros(p.shape[0], q.shape[0], dtype=torch.float64, device=p.device)
+    for k in range(0, p.shape[1], 128):
+        out += (p[:, k:k + 128] @ q[:, k:k + 128].t()).abs()
+    return out
+
+
+def expert_int8(x, w13, s13, w2, s2w):
+    """One int8 expert on tokens x [n, d] (bf16): value and bound of its output rows (fp32).
+
+    Sums. A contraction may be split into S <= 32 parts: each exact int32 part becomes fp32 and takes
+    two scales (3 roundings), and the parts are added (S - 1 roundings), so a sum is off by at most
+    (S + 2) u sum_s |P_s| <= 40 u sum_b |block sums|: relative to the sum itself this grows where the
+    parts cancel.
+    Codes. act is off by ea (the sums of h through silu, the fast activation), its quotient v = act / s2
+    by ea / s2 and by the scale's relative error ds; a code can differ by one where v lies that near to
+    a half."""
+    F = w2.shape[1]
+    u = U[torch.float32]
+    q, sx = quant_int8(x)
+    sh = sx[:, None] * s13.double()[None, :]
+    h = (q @ w13.double().t()) * sh
+    eh = 40 * u * _block_sums(q, w13.double()) * sh
+    g, up, eg, eu = h[:, :F], h[:, F:], eh[:, :F], eh[:, F:]
+    f = activation(g, "silu")[0]
+    a = f * up
+    ef = 1.1 * eg + FAST * f.abs()                    # |silu'| < 1.1
+    ea = ef * (up.abs() + eu) + f.abs() * eu + 4 * u * a.abs()
+    amax = a.abs().amax(dim=1, keepdim=True)
+    s2 = torch.where(amax == 0, torch.ones_like(amax), amax / 127.0)
+    # the largest |act + error| lies within the largest error of any element that can be the largest
+    can = (a.abs() + ea >= (a.abs() - ea).amax(dim=1, keepdim=True)).double()
+    ds = (can * ea).amax(dim=1, keepdim=True) / amax.clamp_min(1e-300) + 2 * u
+    v = a / s2
+    aq = torch.round(v)
+    margin = ea / s2 + (ds + 2 * u) * v.abs()
+    near = ((v.abs() - torch.floor(v.abs()) - 0.5).abs() <= margin * (1 + 1e-3)).double()
+    so = s2 * s2w.double()[None, :]
+    out = (aq @ w2.double().t()) * so
+    flips = (near @ w2.double().abs().t()) * so
+    sums = 40 * u * (_block_sums(aq, w2.double()) * so + flips)
+    return out, flips * (1 + 1e-3) + out.abs() * ds * (1 + 1e-3) + sums

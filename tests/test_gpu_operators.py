@@ -133,3 +133,43 @@ def test_gated_ffn_backward(ops, T, d, F, dtype, act):
         part = ops.moe_gated_ffn_backward(dy, x, w13, w2, h, activation=act, need=need)
         for a, b, want in zip(part, got, need):
             assert torch.equal(a, b) if want else a is None
+
+
+# ------------------------------------------------------------------------------ routed int8 experts
+# (T, d, E, F, k): decode tiles with a K split, ragged groups, experts without a token, prefill
+# tiles of 64 to 256 rows on one CTA and on pairs
+EXPERTS = [(1, 64, 8, 32, 2), (1, 2048, 128, 768, 8), (5, 528, 6, 272, 3), (64, 1024, 16, 528, 4),
+           (300, 528, 4, 336, 2), (700, 272, 3, 2064, 3), (2048, 256, 8, 208, 2)]
+
+
+def routed(T, E, k, g):
+    top, ids = (rnd(g, T, E) + rnd(g, 1, E)).topk(k, dim=1)
+    return ids.to(torch.int32), torch.softmax(top, dim=1)
+
+
+def int8_layer(T, d, E, F, k, seed):
+    g = gen(seed)
+    codes = lambda *n: (rnd(g, *n) * 36).round().clamp(-127, 127).to(torch.int8)  # noqa: E731
+    scale = lambda *n: torch.rand(*n, generator=g, device="cuda") * 1e-3 + 5e-4   # noqa: E731
+    x = rnd(g, T, d).to(torch.bfloat16)
+    ids, w = routed(T, E, k, g)
+    return x, ids, w, codes(E, 2 * F, d), scale(E, 2 * F), codes(E, d, F), scale(E, d)
+
+
+@pytest.mark.parametrize("T,d,E,F,k", EXPERTS)
+def test_grouped_ffn_int8(ops, T, d, E, F, k):
+    x, ids, _, w13, s13, w2, s2 = int8_layer(T, d, E, F, k, T + E)
+    ws = ops.alloc_workspace(ops.dims(T, d, E, F, k))
+    offsets, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F, ws=ws)
+    out, xs = ops.moe_grouped_ffn_int8(x, w13, s13, w2, s2, offsets, perm, k, ws=ws,
+                                       want_act_scale=True)
+    assert ops.device_status(ws) == ops.MOE_OK
+    assert torch.equal(xs.double(), R.quant_int8(x)[1])
+    off = offsets.tolist()
+    for e in range(E):
+        rows = slice(off[e], off[e + 1])
+        if off[e] == off[e + 1]:
+            continue
+        ref = R.expert_int8(x[perm[rows].long()], w13[e], s13[e], w2[e], s2[e])
+        R.check(out[rows], ref, (e, off[e], off[e + 1]))
+    assert (out[off[E]:] == 0).all()
