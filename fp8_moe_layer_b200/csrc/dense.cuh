@@ -41,6 +41,7 @@ struct DenseArgs {
   const uint16_t* h;             // kEpiGatedGrad: h [M][2][N]
   const float *row_scale, *col_scale, *bias;   // kEpiInt8 (bias may be null)
   int* status;
+  int clear_status;              // this launch is the first of its call
 };
 
 // Tile of a launch: `pair` = 256 x 256 on a 2-CTA pair, else 128 x 128 on one CTA.
@@ -58,6 +59,18 @@ bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int t
 bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type);
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s);
+
+// Few tokens (T <= kFewRows): out [T, N] = x [T, K] w[N, K]^T with the epilogues kEpiStore, kEpiInt8,
+// or kEpiGated (w [2N, K], gate rows first; h [T, 2N] when kept). Clears `status` when given.
+constexpr int kFewRows = 16;
+struct FewRowsArgs {
+  const void *x, *w;
+  int T, N, K, type, act;
+  const float *row_scale, *col_scale, *bias;
+  void *out, *h;
+  int* status;
+};
+cudaError_t launch_few_rows(int epi, const FewRowsArgs& args, cudaStream_t s);
 
 // Host helpers of moe_api.cu shared by the entry points.
 bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,

@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "dense_epilogue.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -51,48 +52,6 @@ struct DenseCfg {
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(STAGES >= 4, "pipeline too shallow");
 };
-
-// sigmoid with the fast exponential and division; the exponent is clamped so that the denominator
-// stays finite (relative error ~1e-6, far below the 16-bit rounding that follows).
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.f, 1.f + __expf(fminf(-x, 80.f)));
-}
-
-// f(g) = g s with s = sigmoid(g) (SiLU) or sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3) (GELU,
-// tanh form: 0.5 (1 + tanh z) = sigmoid(2 z)); df = s + g s (1 - s) d(argument)/dg.
-template <bool GRAD>
-__device__ __forceinline__ void gate_fn(int act, float g, float& f, float& df) {
-  constexpr float kC = 1.5957691216057308f;          // 2 sqrt(2 / pi)
-  constexpr float kB = 0.044715f;
-  float arg = g, slope = 1.f;
-  if (act == kActGeluTanh) {
-    const float g2 = g * g;
-    arg = kC * g * fmaf(kB, g2, 1.f);
-    if (GRAD) slope = kC * fmaf(3.f * kB, g2, 1.f);
-  }
-  const float s = sigmoid_fast(arg);
-  f = g * s;
-  if (GRAD) df = fmaf(f * (1.f - s), slope, s);
-}
-
-__device__ __forceinline__ uint32_t pack16(int type, float lo, float hi) {
-  if (type == kBf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ void unpack16(int type, uint32_t w, float& lo, float& hi) {
-  if (type == kBf16) {
-    lo = __uint_as_float(w << 16);
-    hi = __uint_as_float(w & 0xFFFF0000u);
-  } else {
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    lo = v.x;
-    hi = v.y;
-  }
-}
 
 // tile -> product p, m-tile, n-tile: inside a product, groups of 8 m-tiles with m fastest, so the
 // units running at one time share both operands' rows in L2.
@@ -146,6 +105,9 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
   const int total_tiles = args.total_tiles;
   if (unit >= total_tiles) return;                  // (both CTAs of a pair together)
 
+  // the first kernel of a call clears the status word (the first block starts no later than any
+  // other, and a wait reports about a second after its block began)
+  if (args.clear_status && blockIdx.x == 0 && threadIdx.x < 4) args.status[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);

@@ -3,6 +3,7 @@
 //
 //   forward   1. h = x W13^T, act = f(h_gate) h_up           (one kernel, kEpiGated)
 //             2. y = act W2^T                                 (kEpiStore)
+//             (T <= 16: the same two steps by the few-row kernels, few_rows.cu)
 //   backward  1. dy W2, fused with h: dh and act              (one kernel, kEpiGatedGrad)
 //             2. dW13 = dh^T x, dW2 = dy^T act, dx = dh W13   (one launch, longest products first)
 #include <algorithm>
@@ -73,13 +74,37 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   uint8_t* base = static_cast<uint8_t*>(ws);
   int* status = reinterpret_cast<int*>(base);
   uint16_t* act = reinterpret_cast<uint16_t*>(base + p.off_act);
-  if (cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
+
+  if (T <= kFewRows) {
+    FewRowsArgs f{};
+    f.x = x;
+    f.w = w13;
+    f.T = T;
+    f.N = F;
+    f.K = d;
+    f.type = type;
+    f.act = dims->act;
+    f.out = act;
+    f.h = h;
+    f.status = status;
+    if (launch_few_rows(kEpiGated, f, s) != cudaSuccess) return MOE_ERR_CUDA;
+    FewRowsArgs o{};
+    o.x = act;
+    o.w = w2;
+    o.T = T;
+    o.N = d;
+    o.K = F;
+    o.type = type;
+    o.out = y;
+    return launch_few_rows(kEpiStore, o, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
 
   const DenseTile tile = dense_tile(T);
   DenseArgs a{};
   a.n_problems = 1;
   a.type = type;
   a.act = dims->act;
+  a.clear_status = 1;
   a.save_h = h != nullptr;
   a.status = status;
   DenseProblem& g = a.p[0];
@@ -136,8 +161,8 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   int* status = reinterpret_cast<int*>(base);
   uint16_t* act = reinterpret_cast<uint16_t*>(base + p.off_act);
   uint16_t* dh = reinterpret_cast<uint16_t*>(base + p.off_dh);
-  if (cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
-  if (!dx && !dw13 && !dw2) return MOE_OK;
+  if (!dx && !dw13 && !dw2)
+    return cudaMemsetAsync(status, 0, 16, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 
   const DenseTile tile = dense_tile(T);
   DenseArgs a{};
@@ -146,6 +171,7 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   a.act = dims->act;
   a.h = h;
   a.status = status;
+  a.clear_status = 1;
   DenseProblem& g = a.p[0];                        // dL/da = dy W2: W2 [d, F] as it lies
   g.M = T;
   g.N = F;

@@ -184,8 +184,21 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
     if (launch_quant_int8(T, K, x_type, x, q, sx, status, s) != cudaSuccess) return MOE_ERR_CUDA;
     codes = q;
     x_scale = sx;
-  } else if (cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) {
-    return MOE_ERR_CUDA;
+  }
+  if (T <= kFewRows) {
+    FewRowsArgs f{};
+    f.x = codes;
+    f.w = w;
+    f.T = T;
+    f.N = N;
+    f.K = K;
+    f.type = out_type;
+    f.row_scale = x_scale;
+    f.col_scale = w_scale;
+    f.bias = bias;
+    f.out = out;
+    f.status = x ? nullptr : status;
+    return launch_few_rows(kEpiInt8, f, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   const DenseTile tile = dense_tile(T);
   DenseArgs a{};
@@ -203,6 +216,7 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
   a.col_scale = w_scale;
   a.bias = bias;
   a.status = status;
+  a.clear_status = x == nullptr;
   return launch_dense(kEpiInt8, tile, a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

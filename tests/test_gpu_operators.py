@@ -57,7 +57,8 @@ def test_quant_int8_non_finite_rows(ops):
 
 
 # ------------------------------------------------------------------------------ int8 product
-MATMUL = [(1, 16, 16), (1, 4096, 1040), (2, 144, 272), (17, 2064, 528), (128, 512, 256),
+MATMUL = [(1, 16, 16), (1, 4096, 1040), (2, 144, 272), (8, 48, 32), (9, 1040, 48), (16, 272, 144),
+          (3, 528, 19504), (17, 2064, 528), (128, 512, 256),
           (129, 528, 272), (300, 4112, 1040), (1003, 2064, 1040), (2100, 1024, 4144)]
 
 
@@ -93,7 +94,7 @@ def test_matmul_int8_of_codes_extreme_values(ops, T, out_dtype):
 
 
 # ------------------------------------------------------------------------------ gated FFN
-FFN = [(1, 16, 16), (1, 1040, 784), (3, 64, 48), (31, 272, 144), (128, 256, 256), (129, 144, 80),
+FFN = [(1, 16, 16), (1, 1040, 784), (3, 64, 48), (9, 528, 112), (16, 144, 19504), (31, 272, 144), (128, 256, 256), (129, 144, 80),
        (257, 528, 336), (500, 2048, 784), (1000, 1040, 2064)]
 
 
