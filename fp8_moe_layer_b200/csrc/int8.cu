@@ -15,97 +15,242 @@
 
 namespace moe {
 
-// Eight consecutive elements of a row as fp32.
+// Eight consecutive elements of a row as they lie, and as fp32.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* row, int i, float (&v)[8]) {
-  if constexpr (TYPE == kFp32) {
-    const float4* p = static_cast<const float4*>(row) + 2 * i;
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = static_cast<const uint4*>(row)[i];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw8 {
+  uint4 a[TYPE == kFp32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* row, int i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (TYPE == kBf16) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
+    for (int j = 0; j < (TYPE == kFp32 ? 2 : 1); ++j)
+      a[j] = static_cast<const uint4*>(row)[(TYPE == kFp32 ? 2 : 1) * i + j];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < (TYPE == kFp32 ? 2 : 1); ++j) {
+      const uint32_t w[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == kFp32) {
+          v[4 * j + i] = __uint_as_float(w[i]);
+        } else if constexpr (TYPE == kBf16) {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        }
       }
     }
   }
-}
-
-__device__ __forceinline__ uint32_t absmax8(const float (&v)[8], uint32_t m) {
+  __device__ __forceinline__ uint32_t absmax(uint32_t m) const {
+    float v[8];
+    values(v);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return m;
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+};
+
+// Codes of eight values. Eight IEEE divisions cost more than the row's bytes (T = 8192, K = 7168:
+// 65 us with them, HBM 27), so the quotient is first taken as v * inv, inv = 1/s rounded: within
+// 127 * 2^-23 < 2^-16 of fp32(v / s). Adding 1.5 * 2^23 rounds it to an integer, half to even, in the
+// sum's low bits. Where the remainder comes within 2^-13 of a half the two might round apart, and
+// those eight are divided.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float sc, float inv, bool fast) {
+  if (fast) {
+    constexpr float kMagic = 12582912.f;
+    uint32_t t[8];
+    float worst = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float r = fmaf(v[j], inv, kMagic);
+      worst = fmaxf(worst, fabsf(fmaf(v[j], inv, kMagic - r)));
+      t[j] = __float_as_uint(r);
+    }
+    if (worst <= 0.5f - 0.0001220703125f) {
+      const uint32_t p0 = __byte_perm(t[0], t[1], 0x0040), p1 = __byte_perm(t[2], t[3], 0x0040);
+      const uint32_t p2 = __byte_perm(t[4], t[5], 0x0040), p3 = __byte_perm(t[6], t[7], 0x0040);
+      return make_uint2(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410));
+    }
+  }
+  return int8x8(v, sc);
 }
 
-// One block per row (the grid steps over the rows). The first 8192 elements stay in registers
-// between the two passes; longer rows re-read the rest from L1 / L2. HBM-bound for large batches:
-// K bytes x (element size + 1) per row.
-template <int TYPE>
+// Quantises one row with the whole block (BLOCK) or one warp, and returns its scale. The first KEEP
+// vectors of 8 per thread stay in registers between the two passes; longer rows re-read the rest from
+// L1 / L2.
+template <int TYPE, bool BLOCK, int KEEP>
+__device__ __forceinline__ float quantise_row(const void* row, int K, int8_t* codes,
+                                              uint32_t (&red)[8]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  const int tid = BLOCK ? threadIdx.x : lane, step = BLOCK ? blockDim.x : 32;
+  const int nv = K / 8;
+  Raw8<TYPE> raw[KEEP];
+  uint32_t am = 0u;
+#pragma unroll
+  for (int c = 0; c < KEEP; ++c) {
+    const int i = tid + c * step;
+    if (i < nv) raw[c].load(row, i);
+  }
+#pragma unroll
+  for (int c = 0; c < KEEP; ++c)
+    if (tid + c * step < nv) am = raw[c].absmax(am);
+  for (int i = tid + KEEP * step; i < nv; i += step) {
+    Raw8<TYPE> w;
+    w.load(row, i);
+    am = w.absmax(am);
+  }
+  am = __reduce_max_sync(0xffffffffu, am);
+  if constexpr (BLOCK) {
+    __syncthreads();                             // red[] of the previous row has been read
+    if (lane == 0) red[warp] = am;
+    __syncthreads();
+    for (int w = 0; w < nwarps; ++w) am = max(am, red[w]);
+  }
+  const float sc = am == 0u ? 1.f : __fdiv_rn(__uint_as_float(am), 127.f);
+  // (outside this range scale or reciprocal may be subnormal or not finite)
+  const bool fast = am > __float_as_uint(1e-30f) && am < __float_as_uint(1e30f);
+  const float inv = __frcp_rn(sc);
+  uint2* dst = reinterpret_cast<uint2*>(codes);
+  float v[8];
+#pragma unroll
+  for (int c = 0; c < KEEP; ++c) {
+    const int i = tid + c * step;
+    if (i < nv) {
+      raw[c].values(v);
+      dst[i] = codes8(v, sc, inv, fast);
+    }
+  }
+  for (int i = tid + KEEP * step; i < nv; i += step) {
+    Raw8<TYPE> w;
+    w.load(row, i);
+    w.values(v);
+    dst[i] = codes8(v, sc, inv, fast);
+  }
+  return sc;
+}
+
+// Rows of at most 2048 elements that are many go to a warp each: no
+// block barrier between a row's maximum and its codes, eight independent rows per block.
+constexpr int kWarpKeep = 8;
+
+// A block or a warp per row (the grid steps over the rows).
+template <int TYPE, bool BLOCK>
 __global__ void __launch_bounds__(256) quant_int8_kernel(const void* __restrict__ x, int64_t rows,
                                                          int K, int8_t* __restrict__ codes,
                                                          float* __restrict__ scale,
                                                          int* __restrict__ status) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
-  constexpr int kKeep = 4;
   __shared__ uint32_t red[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  const int nv = K / 8;
   if (status && blockIdx.x == 0 && threadIdx.x < 4) status[threadIdx.x] = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  const int64_t r0 = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  for (int64_t r = r0; r < rows; r += BLOCK ? gridDim.x : gridDim.x * 8) {
     const uint8_t* row = static_cast<const uint8_t*>(x) + (size_t)r * K * (TYPE == kFp32 ? 4 : 2);
-    float v[kKeep][8];
-    uint32_t am = 0u;
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
-      if (i < nv) load8<TYPE>(row, i, v[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c)
-      if ((int)(threadIdx.x + c * blockDim.x) < nv) am = absmax8(v[c], am);
-    for (int i = threadIdx.x + kKeep * blockDim.x; i < nv; i += blockDim.x) {
-      float w[8];
-      load8<TYPE>(row, i, w);
-      am = absmax8(w, am);
-    }
-    am = __reduce_max_sync(0xffffffffu, am);
-    __syncthreads();                               // red[] of the previous row has been read
-    if (lane == 0) red[warp] = am;
-    __syncthreads();
-    for (int w = 0; w < nwarps; ++w) am = max(am, red[w]);
-    const float sc = am == 0u ? 1.f : __fdiv_rn(__uint_as_float(am), 127.f);
-    if (threadIdx.x == 0) scale[r] = sc;
-    uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)r * K);
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
-      if (i < nv) dst[i] = int8x8(v[c], sc);
-    }
-    for (int i = threadIdx.x + kKeep * blockDim.x; i < nv; i += blockDim.x) {
-      float w[8];
-      load8<TYPE>(row, i, w);
-      dst[i] = int8x8(w, sc);
-    }
+    const float sc = quantise_row<TYPE, BLOCK, BLOCK ? 4 : kWarpKeep>(row, K, codes + (size_t)r * K, red);
+    if ((BLOCK ? threadIdx.x : threadIdx.x & 31) == 0) scale[r] = sc;
   }
 }
 
 cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8_t* codes,
                               float* scale, int* status, cudaStream_t s) {
-  const int threads = std::min(256, std::max(32, (K / 8 + 31) / 32 * 32));
-  const int grid = (int)std::min<int64_t>(rows, 32LL * num_sms());
-  auto* kernel = type == kBf16 ? quant_int8_kernel<kBf16>
-                 : type == kFp16 ? quant_int8_kernel<kFp16> : quant_int8_kernel<kFp32>;
+  const bool warps = rows >= 8LL * num_sms() && K <= 256 * kWarpKeep;
+  const int threads = warps ? 256 : std::min(256, std::max(32, (K / 8 + 31) / 32 * 32));
+  const int grid = (int)std::min<int64_t>(warps ? (rows + 7) / 8 : rows, 32LL * num_sms());
+  auto* kernel = type == kBf16 ? (warps ? quant_int8_kernel<kBf16, false> : quant_int8_kernel<kBf16, true>)
+                 : type == kFp16 ? (warps ? quant_int8_kernel<kFp16, false> : quant_int8_kernel<kFp16, true>)
+                                 : (warps ? quant_int8_kernel<kFp32, false> : quant_int8_kernel<kFp32, true>);
   launch_pdl(kernel, dim3(grid), dim3(threads), 0, s, x, rows, K, codes, scale, status);
+  return cudaGetLastError();
+}
+
+// Everything the routed int8 FFN needs before its first GEMM, in one launch: block 0 checks the
+// caller's offsets and writes the GEMMs' tile prefix; the others fill the routed rows, clear each row's
+// SwiGLU maximum and zero the output rows behind the last routed one. For few rows a block quantises
+// hidden[perm[r]] straight into row r (no launch for the tokens' codes). For many (COPY), quantising a
+// token once and copying its codes by a warp per row is cheaper than quantising it k times: Qwen3
+// shape, T = 4096, k = 8: 51 us for the latter. An index outside [0, T) gives a zero row and flags
+// MOE_ERR_DEVICE_CHECK.
+template <bool COPY>
+__global__ void __launch_bounds__(256) int8_prepare_kernel(const Int8Prepare a) {
+  pdl_wait();      // predecessor kernel complete, its writes visible
+  pdl_trigger();   // let the next kernel launch
+  __shared__ uint32_t red[8];
+  __shared__ int sums[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (blockIdx.x == 0) {
+    const int per = (a.E + 255) / 256, lo = min(a.E, tid * per), hi = min(a.E, lo + per);
+    int mine = 0, bad = 0;
+    for (int e = lo; e < hi; ++e) {
+      const int p = a.offsets[e], q = a.offsets[e + 1];
+      if (p < 0 || q < p || q > a.rcap) bad = 1;
+      else mine += (q - p + a.BN - 1) / a.BN;
+    }
+    bad = __syncthreads_or(bad);
+    int at = mine;                                 // exclusive prefix over the threads
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += v;
+    }
+    if (lane == 31) sums[warp] = at;
+    __syncthreads();
+    at -= mine;
+    for (int w = 0; w < warp; ++w) at += sums[w];
+    if (bad) {                                     // an empty tile list: no GEMM work is done
+      for (int e = tid; e <= a.E; e += 256) a.tiles[e] = 0;
+      if (tid == 0) report(a.status, kStatusDeviceCheck, kWhereTilePrefix, 0);
+      return;
+    }
+    for (int e = lo; e < hi; ++e) {
+      a.tiles[e] = at;
+      at += (a.offsets[e + 1] - a.offsets[e] + a.BN - 1) / a.BN;
+    }
+    if (lo < hi && hi == a.E) a.tiles[a.E] = at;
+    return;
+  }
+  const int R = (int)min((int64_t)max(a.offsets[a.E], 0), a.rcap);
+  const int me = COPY ? lane : tid, step = COPY ? 32 : 256;
+  const int64_t first = COPY ? (int64_t)(blockIdx.x - 1) * 8 + warp : blockIdx.x - 1;
+  for (int64_t r = first; r < a.rcap; r += (COPY ? 8 : 1) * (int64_t)(gridDim.x - 1)) {
+    if (r >= R) {
+      float4* o = reinterpret_cast<float4*>(a.out + (size_t)r * a.d);
+      for (int i = me; i < a.d / 4; i += step) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      continue;
+    }
+    const int t = a.perm[r];
+    int8_t* dst = a.codes + (size_t)r * a.d;
+    float sc = 0.f;
+    if (t < 0 || t >= a.T) {
+      for (int i = me; i < a.d / 8; i += step) reinterpret_cast<uint2*>(dst)[i] = make_uint2(0u, 0u);
+      if (me == 0) report(a.status, kStatusDeviceCheck, kWhereGather, (int)r);
+    } else if constexpr (COPY) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.token_codes + (size_t)t * a.d);
+#pragma unroll 4
+      for (int i = me; i < a.d / 16; i += step) reinterpret_cast<uint4*>(dst)[i] = src[i];
+      sc = a.token_scale[t];
+    } else {
+      sc = quantise_row<kBf16, true, 4>(a.hidden + (size_t)t * a.d, a.d, dst, red);
+    }
+    if (me == 0) {
+      a.scale[r] = sc;
+      a.amax[r] = 0u;
+    }
+  }
+}
+
+cudaError_t launch_int8_prepare(const Int8Prepare& a, cudaStream_t s) {
+  const bool copy = a.rcap >= 8LL * num_sms();
+  if (copy) {
+    const cudaError_t e = launch_quant_int8(a.T, a.d, kBf16, a.hidden, a.token_codes, a.token_scale,
+                                            nullptr, s);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t blocks = std::max<int64_t>(copy ? (a.rcap + 7) / 8 : a.rcap, 1);
+  const int grid = 1 + (int)std::min<int64_t>(blocks, 32LL * num_sms());
+  launch_pdl(copy ? int8_prepare_kernel<true> : int8_prepare_kernel<false>, dim3(grid), dim3(256), 0,
+             s, a);
   return cudaGetLastError();
 }
 

@@ -188,6 +188,22 @@ cudaError_t launch_ep_dispatch(const Plan& p, int n_ranks, const uint16_t* hidde
 // int8 codes and scales of each row (int8.cu); clears the 16-byte status word when one is given.
 cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8_t* codes,
                               float* scale, int* status, cudaStream_t s);
+// Tile prefix, row codes and scales of the routed int8 FFN (int8.cu).
+struct Int8Prepare {
+  const uint16_t* hidden;         // [T, d] bf16
+  const int32_t *offsets, *perm;  // the caller's, unchecked
+  int T, d, E, BN;
+  int64_t rcap;                   // T * k_max
+  int32_t* tiles;                 // [E + 1]
+  int8_t* token_codes;            // [T, d] and [T]: used for many rows
+  float* token_scale;
+  int8_t* codes;                  // [rcap, d]
+  float* scale;
+  uint32_t* amax;
+  float* out;                     // [rcap, d]: rows >= offsets[E] are zeroed
+  int* status;
+};
+cudaError_t launch_int8_prepare(const Int8Prepare& a, cudaStream_t s);
 
 int num_sms();
 

@@ -468,22 +468,29 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
   q.G = p.E;
   q.Rcap = (int64_t)p.T * p.k_max;
   q.int8 = int8;
-  if (int8)
-    MOE_CUDA(launch_quant_int8(p.T, p.d, kBf16, hidden, reinterpret_cast<int8_t*>(w.xq), w.xs,
-                               nullptr, s));
-  else
+  if (int8) {
+    const Int8Prepare pre{hidden, expert_offsets, perm_token, p.T, p.d, p.E, p.BN, q.Rcap, w.tiles,
+                          reinterpret_cast<int8_t*>(w.xq), w.xs, reinterpret_cast<int8_t*>(w.xqp), w.xsp, w.amax,
+                          expert_out, w.status};
+    MOE_CUDA(launch_int8_prepare(pre, s));
+    if (act_scale_out)
+      MOE_CUDA(launch_quant_int8(p.T, p.d, kBf16, hidden, reinterpret_cast<int8_t*>(w.xq),
+                                 act_scale_out, nullptr, s));
+    w.offsets = const_cast<int32_t*>(expert_offsets);      // read only from here on
+  } else {
     MOE_CUDA(launch_topk_quant(q, nullptr, nullptr, 1, nullptr, nullptr, nullptr, hidden, w.xq,
                                w.xs, false, true, nullptr, w.status, s));
-  if (act_scale_out)
-    MOE_CUDA(cudaMemcpyAsync(act_scale_out, w.xs, sizeof(float) * p.T, cudaMemcpyDeviceToDevice, s));
-  MOE_CUDA(launch_tile_prefix(q, expert_offsets, w.tiles, w.status, s));
-  // the grouped FFN reads offsets/perm from the workspace copies: keep one layout for both paths
-  MOE_CUDA(cudaMemcpyAsync(w.offsets, expert_offsets, sizeof(int32_t) * (p.E + 1),
-                           cudaMemcpyDeviceToDevice, s));
-  MOE_CUDA(cudaMemcpyAsync(w.perm, perm_token, sizeof(int32_t) * q.Rcap, cudaMemcpyDeviceToDevice, s));
+    if (act_scale_out)
+      MOE_CUDA(cudaMemcpyAsync(act_scale_out, w.xs, sizeof(float) * p.T, cudaMemcpyDeviceToDevice, s));
+    MOE_CUDA(launch_tile_prefix(q, expert_offsets, w.tiles, w.status, s));
+    // the grouped FFN reads offsets/perm from the workspace copies: keep one layout for both paths
+    MOE_CUDA(cudaMemcpyAsync(w.offsets, expert_offsets, sizeof(int32_t) * (p.E + 1),
+                             cudaMemcpyDeviceToDevice, s));
+    MOE_CUDA(cudaMemcpyAsync(w.perm, perm_token, sizeof(int32_t) * q.Rcap, cudaMemcpyDeviceToDevice, s));
+  }
   const bool direct = p.g2_splits == 1;
   MOE_TRY(run_ffn(q, w, w13, w13_scale, w2, w2_scale, nullptr, nullptr, nullptr, nullptr,
-                  direct ? expert_out : w.o, (size_t)p.Rpad * p.d, q.Rcap, nullptr, s));
+                  direct ? expert_out : w.o, (size_t)p.Rpad * p.d, q.Rcap, nullptr, s, int8));
   if (!direct)
     MOE_CUDA(launch_reduce_splits(q, w.o, p.g2_splits, (size_t)p.Rpad * p.d, w.offsets + p.E,
                                   expert_out, s));

@@ -256,7 +256,9 @@ def moe_grouped_ffn_int8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets, p
         if perm_token.numel() < T * k_max or not perm_token.is_contiguous():
             raise ValueError("perm_token must be contiguous and hold T * k_max rows")
         ws = alloc_workspace(dm, dev) if ws is None else ws
-        out = torch.zeros(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
+        out = torch.empty(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
+        if T == 0:
+            out.zero_()
         xs = torch.empty(T, dtype=torch.float32, device=dev) if want_act_scale else None
         _check(LIB.moe_grouped_ffn_int8(ctypes.byref(dm), *args, perm_token.data_ptr(),
                                         out.data_ptr(), _p(xs), _p(ws), ws.numel(),

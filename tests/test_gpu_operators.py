@@ -29,7 +29,8 @@ def rnd(g, *n):
 
 # ------------------------------------------------------------------------------ quantisation
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (257, 2064), (5, 8192), (2, 8208), (7, 20000)])
+@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (257, 2064), (5, 8192), (2, 8208), (7, 20000), (1500, 272),
+                                    (2000, 2048)])
 def test_quant_int8_bit_exact(ops, rows, K, dtype):
     g = gen(rows * K)
     x = (rnd(g, rows, K) * torch.exp(2 * rnd(g, rows, 1))).to(DT[dtype])
