@@ -19,11 +19,14 @@
 //
 // Pipeline: TMA (128-byte swizzle) into a ring of stages of 128 bytes of K, one thread issuing
 // tcgen05.mma into double-buffered TMEM accumulators, four epilogue warps; persistent grid, every
-// wait bounded. Two tiles:
+// wait bounded. Tiles (chosen by dense_tile):
 //   pair    256 x 256 on a 2-CTA pair (cta_group::2, M = 256): each CTA stages 128 rows of A and
 //           128 of B per K-block (32 KB) for 256 x 256 of product, so a byte of shared memory
 //           feeds twice the work of a 128 x 128 tile;
-//   single  128 x 128 on one CTA, for at most 128 rows of A.
+//   single  128 x 64, 128 or 256 on one CTA: fewer rows than a pair would fill, or so few tiles that
+//           smaller ones occupy more SMs;
+//   split   a single tile whose K is shared by a cluster of 2, 4 or 8 CTAs, when even those leave SMs
+//           idle: the partial sums meet through distributed shared memory, no workspace, no counters.
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,10 +36,9 @@
 
 namespace moe {
 
-template <int EPI, bool PAIR>
+template <int EPI, bool PAIR, int BN, bool SPLIT>
 struct DenseCfg {
   static constexpr bool I8 = EPI == kEpiInt8;
-  static constexpr int BN = PAIR ? 256 : 128;
   static constexpr int NB = PAIR ? BN / 2 : BN;      // rows of B staged by one CTA
   static constexpr int KE = I8 ? 128 : 64;           // elements of K per stage (128 bytes)
   static constexpr int A_BYTES = 128 * 128;
@@ -47,10 +49,15 @@ struct DenseCfg {
   static constexpr int BUFS = (EPI == kEpiGated || EPI == kEpiGatedGrad) ? 3 : 2;
   static constexpr int STG_BYTES = 4 * BUFS * 4096;
   static constexpr int SMEM_MAX = 232448;
-  static constexpr int STAGES = (SMEM_MAX - 1024 - STG_BYTES - 256) / STAGE_BYTES;
+  static constexpr int FIT = (SMEM_MAX - 1024 - STG_BYTES - 256) / STAGE_BYTES;
+  static constexpr int STAGES = FIT > 12 ? 12 : FIT;
   static constexpr int SMEM = 1024 + STG_BYTES + STAGES * STAGE_BYTES + 256;
   static constexpr int TMEM_COLS = 2 * BN;
-  static_assert(STAGES >= 4, "pipeline too shallow");
+  static_assert(STAGES >= 3, "pipeline too shallow");
+  static_assert(!PAIR || (BN == 256 && !SPLIT), "pair tiles");
+  static_assert(EPI != kEpiGated || BN >= 128, "a gated tile stages 64 features at a time");
+  // a split tile's partial sums wait in the (by then idle) stages
+  static_assert(!SPLIT || STAGES * STAGE_BYTES >= 128 * BN * 4, "exchange buffer");
 };
 
 // tile -> product p, m-tile, n-tile: inside a product, groups of 8 m-tiles with m fastest, so the
@@ -79,12 +86,137 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, int piece0,
         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-template <int EPI, bool PAIR>
+__device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Sixteen consecutive columns (at `col`) of `row`, rounded to 16 bits or as fp32.
+__device__ __forceinline__ void store16_cols(void* out, int type, int64_t ld, int row, int col,
+                                             const float (&v)[16]) {
+  if (type == kFp32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ld + col);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack16(type, v[2 * i], v[2 * i + 1]);
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * ld + col);
+    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// The epilogue of a split tile: CTA s of the cluster takes the s-th share of the tile's columns (in
+// steps of 16), adds the CTAs' partial sums from their shared memory in rank order (the result does
+// not depend on timing) and stores directly: few bytes per CTA, and a share may be narrower than a
+// staged row.
+template <int EPI, int BN>
+__device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, int split, int srank,
+                                               uint8_t* parked) {
+  constexpr bool I8 = EPI == kEpiInt8;
+  constexpr int COLS = EPI == kEpiGated ? BN / 2 : BN;   // output columns of the tile
+  int pi, mt, nt;
+  dense_tile_at(args, tile, pi, mt, nt);
+  const DenseProblem& P = args.p[pi];
+  const int rl = (threadIdx.x - 128);                // row of the tile
+  const int row = mt * 128 + rl;
+  if (row >= P.M) return;
+  const uint32_t base = smem_addr(parked);
+  auto sum16 = [&](int c, float (&v)[16]) {
+    int acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = 0.f;
+      acc[i] = 0;
+    }
+    for (int s = 0; s < split; ++s) {
+      uint32_t remote;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base), "r"(s));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 p = ld_cluster16(remote + (((c / 4 + i) * 128 + rl) << 4));
+        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (I8) acc[4 * i + e] += static_cast<int>(w[e]);
+          else v[4 * i + e] += __uint_as_float(w[e]);
+        }
+      }
+    }
+    if constexpr (I8) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(acc[i]);
+    }
+  };
+  const int64_t N = P.N;
+  for (int g = srank; g < COLS / 16; g += split) {
+    const int c = 16 * g, col = nt * COLS + c;
+    if (col >= P.N) continue;
+    float v[16];
+    sum16(c, v);
+    if constexpr (EPI == kEpiStore) {
+      store16_cols(P.out_ptr, args.type, N, row, col, v);
+    } else if constexpr (EPI == kEpiInt8) {
+      const float rs = args.row_scale[row];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] *= rs * __ldg(args.col_scale + col + i);
+        if (args.bias) v[i] += __ldg(args.bias + col + i);
+      }
+      store16_cols(P.out_ptr, args.type, N, row, col, v);
+    } else if constexpr (EPI == kEpiGated) {
+      float u[16], act[16], unused;
+      sum16(COLS + c, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        gate_fn<false>(args.act, v[i], act[i], unused);
+        act[i] *= u[i];
+      }
+      store16_cols(P.out_ptr, args.type, N, row, col, act);
+      if (args.save_h) {
+        store16_cols(P.out_h_ptr, args.type, 2 * N, row, col, v);
+        store16_cols(P.out_h_ptr, args.type, 2 * N, row, static_cast<int>(N) + col, u);
+      }
+    } else {
+      float act[16], dg[16], du[16];
+      const uint4* hg = reinterpret_cast<const uint4*>(args.h + (int64_t)row * 2 * N + col);
+      const uint4* hu = reinterpret_cast<const uint4*>(args.h + (int64_t)row * 2 * N + N + col);
+      const uint4 gw[2] = {__ldg(hg), __ldg(hg + 1)}, uw[2] = {__ldg(hu), __ldg(hu + 1)};
+      const uint32_t* gp = reinterpret_cast<const uint32_t*>(gw);
+      const uint32_t* up = reinterpret_cast<const uint32_t*>(uw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float g2[2], u2[2];
+        unpack16(args.type, gp[i], g2[0], g2[1]);
+        unpack16(args.type, up[i], u2[0], u2[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float f, df;
+          gate_fn<true>(args.act, g2[e], f, df);
+          const int k = 2 * i + e;
+          act[k] = f * u2[e];
+          dg[k] = v[k] * u2[e] * df;
+          du[k] = v[k] * f;
+        }
+      }
+      store16_cols(P.out_ptr, args.type, N, row, col, act);
+      store16_cols(P.out_h_ptr, args.type, 2 * N, row, col, dg);
+      store16_cols(P.out_h_ptr, args.type, 2 * N, row, static_cast<int>(N) + col, du);
+    }
+  }
+}
+
+template <int EPI, bool PAIR, int BN, bool SPLIT>
 __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constant__ DenseArgs args) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
-  using C = DenseCfg<EPI, PAIR>;
-  constexpr int BN = C::BN;
+  using C = DenseCfg<EPI, PAIR, BN, SPLIT>;
   constexpr bool kGatedCols = EPI == kEpiGated;     // B tile = BN/2 gate rows + BN/2 up rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -100,8 +232,11 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = PAIR ? cluster_rank() : 0u;
   const bool leader = crank == 0;
-  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  // A split tile: a cluster of args.split CTAs shares it, CTA s taking the s-th part of K.
+  const int split = SPLIT ? args.split : 1;
+  const int srank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
+  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x) / split;
+  const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x) / split;
   const int total_tiles = args.total_tiles;
   if (unit >= total_tiles) return;                  // (both CTAs of a pair together)
 
@@ -128,6 +263,10 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       tmem_alloc(tmem_slot, C::TMEM_COLS);
       tmem_relinquish();
     }
+  }
+  if (warp == 3 && lane < args.n_problems) {
+    tma_prefetch_map(&args.p[lane].a);
+    tma_prefetch_map(&args.p[lane].b);
   }
   tc_fence_before_sync();
   if constexpr (PAIR) cluster_sync_all();
@@ -160,8 +299,10 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         const DenseProblem& P = args.p[pi];
         const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128;
         const int n0 = nt * BN + static_cast<int>(crank) * C::NB;
-        const int a_mn = P.a_mn, b_mn = P.b_mn, num_kb = P.num_kb;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        const int a_mn = P.a_mn, b_mn = P.b_mn;
+        const int kb0 = SPLIT ? P.num_kb * srank / split : 0;
+        const int kb1 = SPLIT ? P.num_kb * (srank + 1) / split : P.num_kb;
+        for (int kb = kb0; kb < kb1; ++kb) {
           const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
                                 : mbar_wait(&empty[stage], phase ^ 1u);
           if (!got) {
@@ -171,7 +312,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           }
           uint8_t* sa = stages + stage * C::STAGE_BYTES;
           uint8_t* sb = sa + C::A_BYTES;
-          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * C::STAGE_BYTES);
+          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (P.a_rows * 128 + C::B_BYTES));
           if (!C::I8 && a_mn) {
             load2(sa, &P.a, stage, m0, kb * 64, pol);
             load2(sa + 8192, &P.a, stage, m0 + 64, kb * 64, pol);
@@ -226,7 +367,8 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         int pi, mt, nt;
         dense_tile_at(args, tile, pi, mt, nt);
         const int a_mn = C::I8 ? 0 : args.p[pi].a_mn, b_mn = C::I8 ? 0 : args.p[pi].b_mn;
-        const int num_kb = args.p[pi].num_kb;
+        const int kb0 = SPLIT ? args.p[pi].num_kb * srank / split : 0;
+        const int kb1 = SPLIT ? args.p[pi].num_kb * (srank + 1) / split : args.p[pi].num_kb;
         const uint32_t idesc =
             C::I8 ? idesc_s8_s32(PAIR ? 256 : 128, BN)
                   : idesc_f16_f32(args.type == kBf16, PAIR ? 256 : 128, BN, a_mn, b_mn);
@@ -242,7 +384,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         const uint32_t d_tmem = tmem_base + buf * BN;
         // descriptor steps of one MMA's K (32 bytes of a row, or 16 rows of 128 bytes), in 16 bytes
         const uint64_t astep = a_mn ? 128u : 2u, bstep = b_mn ? 128u : 2u;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&full[stage], phase)) {
             report(args.status, kStatusDeviceTimeout, kWhereDense, 3);
             ok = false;
@@ -257,10 +399,10 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           for (int kk = 0; kk < 4; ++kk) {
             if constexpr (C::I8)
               mma_i8<PAIR>(d_tmem, adesc + astep * kk, bdesc + bstep * kk, idesc,
-                           (kb > 0 || kk > 0) ? 1u : 0u);
+                           (kb > kb0 || kk > 0) ? 1u : 0u);
             else
               mma_f16<PAIR>(d_tmem, adesc + astep * kk, bdesc + bstep * kk, idesc,
-                            (kb > 0 || kk > 0) ? 1u : 0u);
+                            (kb > kb0 || kk > 0) ? 1u : 0u);
           }
           if constexpr (PAIR) {
             mma_commit_pair(empty_l + 8u * stage);
@@ -311,6 +453,23 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       }
       tc_fence_after_sync();
       const uint32_t tbase = tmem_base + buf * BN + (static_cast<uint32_t>(32 * q) << 16);
+      if constexpr (SPLIT) {
+        // Park this CTA's partial sums in shared memory (column group of 4, row: a warp's 16-byte
+        // pieces are consecutive); the reduction follows the cluster barrier below.
+        if (rows_any) {
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tbase + c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(stages + (((c / 4 + i) * 128 + 32 * q + lane) << 4)) =
+                  make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          }
+        }
+        break;                                       // one tile per cluster
+      }
       auto load32 = [&](int c, uint32_t (&r)[32]) {
         tmem_ld16(tbase + c, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
         tmem_ld16(tbase + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
@@ -482,8 +641,13 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
     if (lane == 0) bulk_wait_all();                  // this warp's stores have completed
   }
 
+  if constexpr (SPLIT) {
+    // Every thread of the cluster passes both barriers, also after a timeout.
+    cluster_sync_all();                              // all partial sums are parked
+    if (warp >= 4) split_epilogue<EPI, BN>(args, unit, split, srank, stages);
+  }
   tc_fence_before_sync();
-  if constexpr (PAIR) cluster_sync_all();
+  if constexpr (PAIR || SPLIT) cluster_sync_all();   // (no CTA leaves while another reads its sums)
   else __syncthreads();
   if (warp == 2) {
     tc_fence_after_sync();
@@ -498,12 +662,50 @@ static CUtensorMapDataType map_type(int type) {
          : type == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 }
 
-DenseTile dense_tile(int64_t M) { return DenseTile{M > 128}; }
+// The launch's tile, by an estimate of its time in cycles of one CTA. A K-block (128 bytes of K) costs a
+// CTA the staging of its rows of A and B (about 2.1 cycles per 128-byte row: 60 bytes a cycle from L2)
+// or its MMAs, whichever is longer; the launch costs its busiest unit's K-blocks plus one epilogue.
+DenseTile dense_tile(int epi, const int (*mnk)[3], int n) {
+  const int kb_elems = epi == kEpiInt8 ? 128 : 64;
+  DenseTile best{};
+  double best_cost = 0.0;
+  auto consider = [&](bool pair, int bn, int split) {
+    const int units = pair ? kPlanSMs / 2 : kPlanSMs / split;
+    const int bm = pair ? 256 : 128, cols = epi == kEpiGated ? bn / 2 : bn;
+    int64_t tiles = 0, work = 0, longest = 0, rows = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t t = (int64_t)((mnk[i][0] + bm - 1) / bm) * ((mnk[i][1] + cols - 1) / cols);
+      const int64_t kb = (mnk[i][2] + kb_elems - 1) / kb_elems;
+      tiles += t;
+      work += t * kb;
+      longest = std::max(longest, kb);
+      rows = std::max<int64_t>(rows, mnk[i][0]);
+    }
+    if (split > 1 && longest < 4 * split) return;
+    const double a_rows = std::min<double>(128, rows);
+    const double kb_cost = pair ? 540.0 : std::max(2.1 * (a_rows + bn), 2.0 * bn);
+    const int64_t waves = (tiles + units - 1) / units;
+    // one product: whole waves of its tiles; several: the mean load, or the longest tile
+    const double kbs = n == 1 ? (double)waves * longest / split
+                              : std::max<double>((double)work / units + 0.5 * longest, longest);
+    if (split > 1 && waves > 1) return;              // a split launch is not persistent
+    const double cost = kbs * kb_cost + 10.0 * bn + (split > 1 ? 1500.0 + 300.0 * split : 0.0);
+    if (best_cost == 0.0 || cost < best_cost * (1.0 - 1e-9)) {
+      best_cost = cost;
+      best = DenseTile{pair, bn, split};
+    }
+  };
+  consider(true, 256, 1);
+  for (int bn = 256; bn >= (epi == kEpiGated ? 128 : 64); bn /= 2) {
+    consider(false, bn, 1);
+    if (n == 1 && bn <= 128)
+      for (int split = 2; split <= 8; split *= 2) consider(false, bn, split);
+  }
+  return best;
+}
 
 bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
-                       int type, bool mn, bool is_a, bool pair) {
-  (void)is_a;
-  (void)pair;       // both tiles stage 128 rows of either operand per CTA
+                       int type, bool mn, bool is_a, DenseTile tile) {
   if (mn) {         // [K][rows]: box 64 elements x 64 of K
     const uint64_t dims[2] = {(uint64_t)rows, (uint64_t)K};
     const uint64_t str[1] = {(uint64_t)rows * type_bytes};
@@ -512,15 +714,18 @@ bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K
   }
   const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
   const uint64_t str[1] = {(uint64_t)K * type_bytes};
-  const uint32_t box[2] = {(uint32_t)(128 / type_bytes), 128};
+  const uint32_t box[2] = {(uint32_t)(128 / type_bytes),
+                           is_a ? (uint32_t)dense_a_rows(rows)
+                                : (uint32_t)(tile.pair ? tile.bn / 2 : tile.bn)};
   return make_map(m, base, 2, dims, str, box,
                   type_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(type));
 }
 
-bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, bool pair) {
+bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type,
+                             DenseTile tile) {
   const uint64_t dims[3] = {(uint64_t)K, (uint64_t)F, 2};
   const uint64_t str[2] = {(uint64_t)K * 2, (uint64_t)F * K * 2};
-  const uint32_t box[3] = {64, pair ? 128u : 64u, 1};
+  const uint32_t box[3] = {64, (uint32_t)tile.bn / 2, 1};
   return make_map(m, w13, 3, dims, str, box, map_type(type));
 }
 
@@ -540,16 +745,16 @@ bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F
 }
 
 namespace {
-template <int EPI, bool PAIR>
+template <int EPI, bool PAIR, int BN, bool SPLIT>
 cudaError_t launch_dense_t(const DenseArgs& args, cudaStream_t s) {
-  using C = DenseCfg<EPI, PAIR>;
+  using C = DenseCfg<EPI, PAIR, BN, SPLIT>;
   static int unit_cache[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64) return cudaErrorInvalidDevice;
   if (!unit_cache[dev]) {
-    err = cudaFuncSetAttribute(dense_gemm_kernel<EPI, PAIR>,
+    err = cudaFuncSetAttribute(dense_gemm_kernel<EPI, PAIR, BN, SPLIT>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (err != cudaSuccess) return err;
     int units = num_sms();
@@ -566,31 +771,46 @@ cudaError_t launch_dense_t(const DenseArgs& args, cudaStream_t s) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int clusters = 0;
-      err = cudaOccupancyMaxActiveClusters(&clusters, dense_gemm_kernel<EPI, PAIR>, &cfg);
+      err = cudaOccupancyMaxActiveClusters(&clusters, dense_gemm_kernel<EPI, PAIR, BN, SPLIT>, &cfg);
       if (err != cudaSuccess) return err;
       if (clusters < 1) return cudaErrorInvalidConfiguration;
       units = std::min(clusters, num_sms() / 2);
     }
     unit_cache[dev] = units;
   }
-  const int units = std::min(unit_cache[dev], args.total_tiles);
-  launch_pdl_cluster(dense_gemm_kernel<EPI, PAIR>, dim3(PAIR ? 2 * units : units), dim3(256),
-                     C::SMEM, PAIR ? 2 : 1, s, args);
+  const int units = SPLIT ? args.total_tiles : std::min(unit_cache[dev], args.total_tiles);
+  const int cluster = PAIR ? 2 : SPLIT ? args.split : 1;
+  launch_pdl_cluster(dense_gemm_kernel<EPI, PAIR, BN, SPLIT>, dim3(units * cluster), dim3(256), C::SMEM,
+                     cluster, s, args);
   return cudaGetLastError();
 }
 
 template <int EPI>
 cudaError_t launch_dense_e(DenseTile tile, const DenseArgs& args, cudaStream_t s) {
-  return tile.pair ? launch_dense_t<EPI, true>(args, s) : launch_dense_t<EPI, false>(args, s);
+  if (tile.pair) return launch_dense_t<EPI, true, 256, false>(args, s);
+  if (tile.split > 1) {
+    if (tile.bn == 128) return launch_dense_t<EPI, false, 128, true>(args, s);
+    if constexpr (EPI != kEpiGated) return launch_dense_t<EPI, false, 64, true>(args, s);
+    return cudaErrorInvalidValue;
+  }
+  switch (tile.bn) {
+    case 256: return launch_dense_t<EPI, false, 256, false>(args, s);
+    case 128: return launch_dense_t<EPI, false, 128, false>(args, s);
+    default:
+      if constexpr (EPI != kEpiGated) return launch_dense_t<EPI, false, 64, false>(args, s);
+      return cudaErrorInvalidValue;
+  }
 }
 }  // namespace
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s) {
-  const int bm = tile.pair ? 256 : 128, bn = tile.pair ? 256 : 128;
-  const int cols = epi == kEpiGated ? bn / 2 : bn;
+  const int bm = tile.pair ? 256 : 128, cols = epi == kEpiGated ? tile.bn / 2 : tile.bn;
+  args.split = tile.split;
   int64_t total = 0;
   for (int i = 0; i < args.n_problems; ++i) {
     DenseProblem& p = args.p[i];
+    // A's boxes: 128 rows, or fewer when all of A has fewer (MN-major boxes are always whole)
+    p.a_rows = p.a_mn ? 128 : (int)dense_a_rows(p.M);
     p.m_tiles = (p.M + bm - 1) / bm;
     p.n_tiles = (p.N + cols - 1) / cols;
     p.num_kb = epi == kEpiInt8 ? (p.K + 127) / 128 : (p.K + 63) / 64;

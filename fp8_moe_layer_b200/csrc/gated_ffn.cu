@@ -99,7 +99,8 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
     return launch_few_rows(kEpiStore, o, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
 
-  const DenseTile tile = dense_tile(T);
+  const int mnk1[1][3] = {{T, F, d}}, mnk2[1][3] = {{T, d, F}};
+  DenseTile tile = dense_tile(kEpiGated, mnk1, 1);
   DenseArgs a{};
   a.n_problems = 1;
   a.type = type;
@@ -108,26 +109,30 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   a.save_h = h != nullptr;
   a.status = status;
   DenseProblem& g = a.p[0];
+  g.out_ptr = act;
+  g.out_h_ptr = h;
   g.M = T;
   g.N = F;
   g.K = d;
-  if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile.pair) ||
-      !dense_map_gated_weights(&g.b, w13, F, d, type, tile.pair) ||
+  if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile) ||
+      !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
       !dense_map_out(&g.out, act, T, F, type) ||
       !dense_map_out_halves(&g.out_h, h ? h : act, T, h ? F : F / 2, type))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
+  tile = dense_tile(kEpiStore, mnk2, 1);
   DenseArgs b{};
   b.n_problems = 1;
   b.type = type;
   b.status = status;
   DenseProblem& o = b.p[0];
+  o.out_ptr = y;
   o.M = T;
   o.N = d;
   o.K = F;
-  if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile.pair) ||
-      !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile.pair) ||
+  if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile) ||
+      !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile) ||
       !dense_map_out(&o.out, y, T, d, type))
     return MOE_ERR_UNSUPPORTED;
   return launch_dense(kEpiStore, tile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -164,7 +169,8 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   if (!dx && !dw13 && !dw2)
     return cudaMemsetAsync(status, 0, 16, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 
-  const DenseTile tile = dense_tile(T);
+  const int mnk1[1][3] = {{T, F, d}};
+  const DenseTile tile = dense_tile(kEpiGatedGrad, mnk1, 1);
   DenseArgs a{};
   a.n_problems = 1;
   a.type = type;
@@ -173,39 +179,51 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   a.status = status;
   a.clear_status = 1;
   DenseProblem& g = a.p[0];                        // dL/da = dy W2: W2 [d, F] as it lies
+  g.out_ptr = act;
+  g.out_h_ptr = dh;
   g.M = T;
   g.N = F;
   g.K = d;
   g.b_mn = 1;
-  if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile.pair) ||
-      !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile.pair) ||
+  if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile) ||
+      !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile) ||
       !dense_map_out(&g.out, act, T, F, type) || !dense_map_out_halves(&g.out_h, dh, T, F, type))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
-  // The three products that follow are one launch: together they fill the last wave better.
+  // The products that follow are one launch, the longest K first: together they fill the last wave
+  // better than three.
   struct Product {
     const void *a, *b;
     void* out;
     int M, N, K, a_mn;
   };
-  const Product all[3] = {{dh, x, dw13, 2 * F, d, T, 1},
-                          {dy, act, dw2, d, F, T, 1},
-                          {dh, w13, dx, T, d, 2 * F, 0}};
+  Product all[3] = {{dh, x, dw13, 2 * F, d, T, 1},
+                    {dy, act, dw2, d, F, T, 1},
+                    {dh, w13, dx, T, d, 2 * F, 0}};
+  if (2 * F > T) std::rotate(all, all + 2, all + 3);
+  // (the tile goes by all three sizes, so a gradient does not depend on which others are wanted)
+  int sizes[3][3];
+  for (int i = 0; i < 3; ++i) {
+    sizes[i][0] = all[i].M;
+    sizes[i][1] = all[i].N;
+    sizes[i][2] = all[i].K;
+  }
+  const DenseTile wtile = dense_tile(kEpiStore, sizes, 3);
   DenseArgs b{};
   b.type = type;
   b.status = status;
-  const DenseTile wtile{true};
   for (const Product& pr : all) {
     if (!pr.out) continue;
     DenseProblem& o = b.p[b.n_problems++];
     o.M = pr.M;
     o.N = pr.N;
     o.K = pr.K;
+    o.out_ptr = pr.out;
     o.a_mn = pr.a_mn;
     o.b_mn = 1;
-    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, true) ||
-        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, true) ||
+    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, wtile) ||
+        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, wtile) ||
         !dense_map_out(&o.out, pr.out, pr.M, pr.N, type))
       return MOE_ERR_UNSUPPORTED;
   }

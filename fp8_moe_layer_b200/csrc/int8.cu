@@ -345,13 +345,15 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
     f.status = x ? nullptr : status;
     return launch_few_rows(kEpiInt8, f, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
-  const DenseTile tile = dense_tile(T);
+  const int mnk[1][3] = {{T, N, K}};
+  const DenseTile tile = dense_tile(kEpiInt8, mnk, 1);
   DenseArgs a{};
   DenseProblem& d = a.p[0];
-  if (!dense_map_operand(&d.a, codes, T, K, 1, 0, false, true, tile.pair) ||
-      !dense_map_operand(&d.b, w, N, K, 1, 0, false, false, tile.pair) ||
+  if (!dense_map_operand(&d.a, codes, T, K, 1, 0, false, true, tile) ||
+      !dense_map_operand(&d.b, w, N, K, 1, 0, false, false, tile) ||
       !dense_map_out(&d.out, out, T, N, out_type))
     return MOE_ERR_UNSUPPORTED;
+  d.out_ptr = out;
   d.M = T;
   d.N = N;
   d.K = K;
