@@ -67,15 +67,20 @@ bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s);
 
 // Few tokens (T <= kFewRows): out [T, N] = x [T, K] w[N, K]^T with the epilogues kEpiStore, kEpiInt8,
-// or kEpiGated (w [2N, K], gate rows first; h [T, 2N] when kept). Clears `status` when given.
+// or kEpiGated (w [2N, K], gate rows first; h [T, 2N] when kept).
 constexpr int kFewRows = 16;
 struct FewRowsArgs {
   const void *x, *w;
   int T, N, K, type, act;
+  int x_type;                    // kEpiInt8: -1 x holds codes (row_scale), else x is quantised here
   const float *row_scale, *col_scale, *bias;
   void *out, *h;
   int* status;
+  int clear_status;              // this launch is the first of its call
+  int x_stride;                  // set by launch_few_rows: pitch of x in shared memory, 0 = left in L2
 };
+// Whether kEpiInt8 can quantise T tokens of K elements itself.
+bool few_rows_quantises(int T, int K);
 cudaError_t launch_few_rows(int epi, const FewRowsArgs& args, cudaStream_t s);
 
 // Host helpers of moe_api.cu shared by the entry points.

@@ -87,6 +87,7 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
     f.out = act;
     f.h = h;
     f.status = status;
+    f.clear_status = 1;
     if (launch_few_rows(kEpiGated, f, s) != cudaSuccess) return MOE_ERR_CUDA;
     FewRowsArgs o{};
     o.x = act;
@@ -96,6 +97,7 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
     o.K = F;
     o.type = type;
     o.out = y;
+    o.status = status;
     return launch_few_rows(kEpiStore, o, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
 
