@@ -26,7 +26,7 @@ struct DenseProblem {
   CUtensorMap a, b;
   CUtensorMap out;               // D (kEpiStore, kEpiInt8), act (the gated ones)
   CUtensorMap out_h;             // h or dh as [M][2][N] (the gated ones)
-  void *out_ptr, *out_h_ptr;     // the same tensors, for a split tile's direct stores
+  CUtensorMap out16, out_h16;    // the same with 16-column boxes (split tiles, odd widths)
   int M, N, K;                   // valid sizes; gated: N = F (gate and up columns each)
   int a_mn, b_mn;                // 1: the operand's contraction index is outermost
   int m_tiles, n_tiles, num_kb, a_rows;  // set by launch_dense
@@ -37,7 +37,7 @@ constexpr int kMaxProblems = 3;
 struct DenseArgs {
   DenseProblem p[kMaxProblems];
   int n_problems, total_tiles;
-  int split;                     // set by launch_dense
+  int split, bn, direct;         // set by launch_dense
   int type, act;                 // 16-bit operands and outputs; int8: the output's type
   int save_h;                    // kEpiGated: write h
   const uint16_t* h;             // kEpiGatedGrad: h [M][2][N]
@@ -46,10 +46,12 @@ struct DenseArgs {
   int clear_status;              // this launch is the first of its call
 };
 
-// Tile of a launch: 256 x 256 on a 2-CTA pair, or 128 x bn on one CTA, its K split over `split` CTAs.
+// Tile of a launch: 256 x 256 on a 2-CTA pair, or 128 x bn on one CTA, its K split over `split` CTAs;
+// `direct`: one product of one m-tile, whose outputs leave in steps of 16 columns (any such bn).
 struct DenseTile {
   bool pair;
   int bn, split;
+  bool direct;
 };
 // The tile for a launch of n products of sizes {M, N, K} (gated: N = F) with epilogue `epi`.
 DenseTile dense_tile(int epi, const int (*mnk)[3], int n);
@@ -59,10 +61,10 @@ inline int64_t dense_a_rows(int64_t M) { return M >= 128 ? 128 : (M + 15) / 16 *
 // Tensor maps of one operand. rows x K elements of `bytes` (2 or 1) bytes, K-major unless mn.
 bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
                        int type, bool mn, bool is_a, DenseTile tile);
-// Gated weights [2][F][K] and output maps [M][N] / [M][2][N].
+// Gated weights [2][F][K].
 bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, DenseTile tile);
-bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type);
-bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type);
+// Output maps of a problem: out [M][N] and, for the gated epilogues, h or dh [M][2][N] (or null).
+bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, void* halves);
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s);
 

@@ -25,6 +25,7 @@
 //           feeds twice the work of a 128 x 128 tile;
 //   single  128 x 64, 128 or 256 on one CTA: fewer rows than a pair would fill, or so few tiles that
 //           smaller ones occupy more SMs;
+//           (for at most 128 rows of A any multiple of 16 columns that deals the columns out evenly);
 //   split   a single tile whose K is shared by a cluster of 2, 4 or 8 CTAs, when even those leave SMs
 //           idle: the partial sums meet through distributed shared memory, no workspace, no counters.
 #include <algorithm>
@@ -95,38 +96,122 @@ __device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
   return v;
 }
 
-// Sixteen consecutive columns (at `col`) of `row`, rounded to 16 bits or as fp32.
-__device__ __forceinline__ void store16_cols(void* out, int type, int64_t ld, int row, int col,
-                                             const float (&v)[16]) {
+// Sixteen columns of this lane's row into a staging slot of dense rows (32 bytes of 16 bits, 64 of fp32).
+__device__ __forceinline__ void stage16(uint8_t* slot, int type, int lane, const float (&v)[16]) {
   if (type == kFp32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ld + col);
+    float4* o = reinterpret_cast<float4*>(slot + lane * 64);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack16(type, v[2 * i], v[2 * i + 1]);
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * ld + col);
+    uint4* o = reinterpret_cast<uint4*>(slot + lane * 32);
     o[0] = make_uint4(w[0], w[1], w[2], w[3]);
     o[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
+// Sixteen gate and sixteen up pre-activations of a row of h [M][2][N].
+__device__ __forceinline__ void load_h16(const uint16_t* h, int N, int64_t row, int col, uint4 (&v)[4]) {
+  const uint4* g = reinterpret_cast<const uint4*>(h + row * 2 * N + col);
+  const uint4* u = reinterpret_cast<const uint4*>(h + row * 2 * N + N + col);
+  v[0] = __ldg(g);
+  v[1] = __ldg(g + 1);
+  v[2] = __ldg(u);
+  v[3] = __ldg(u + 1);
+}
+
+// Sixteen columns of a warp's 32 rows from row0 on: epilogue, staging and TMA stores through the maps
+// with 16-column boxes (clipped behind the last row). v: the accumulators (int8: the exact int32 sum as
+// fp32), u: the up columns (kEpiGated); rs, and cl, bl of lane i (i + 16): the row's scale and column
+// i's scale and bias (kEpiInt8); h: the row's 16 gate and 16 up pre-activations (kEpiGatedGrad). `buf`:
+// this warp's staging, two slots taken in turn by `n`.
+template <int EPI>
+__device__ __forceinline__ void finish16(const DenseArgs& args, const DenseProblem& P, int row0, int lane,
+                                         int col, float rs, float cl, float bl,
+                                         const uint4 (&h)[4], float (&v)[16], const float (&u)[16],
+                                         uint8_t* buf, int& n) {
+  constexpr bool kTwoHalves = EPI == kEpiGated || EPI == kEpiGatedGrad;
+  uint8_t* slot = buf + (n++ & 1) * (kTwoHalves ? 4096 : 2048);
+  float w0[16], w1[16], w2[16];                      // output, and the two halves of h or dh
+  if constexpr (EPI == kEpiStore) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w0[i] = v[i];
+  } else if constexpr (EPI == kEpiInt8) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      w0[i] = v[i] * (rs * __shfl_sync(0xffffffffu, cl, i, 16));
+      if (args.bias) w0[i] += __shfl_sync(0xffffffffu, bl, i, 16);
+    }
+  } else if constexpr (EPI == kEpiGated) {
+    float unused;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      gate_fn<false>(args.act, v[i], w0[i], unused);
+      w0[i] *= u[i];
+      w1[i] = v[i];
+      w2[i] = u[i];
+    }
+  } else {
+    const uint32_t* gp = reinterpret_cast<const uint32_t*>(h);
+    const uint32_t* up = reinterpret_cast<const uint32_t*>(h + 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float g2[2], u2[2];
+      unpack16(args.type, gp[i], g2[0], g2[1]);
+      unpack16(args.type, up[i], u2[0], u2[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float f, df;
+        gate_fn<true>(args.act, g2[e], f, df);
+        const int k = 2 * i + e;
+        w0[k] = f * u2[e];
+        w1[k] = v[k] * u2[e] * df;
+        w2[k] = v[k] * f;
+      }
+    }
+  }
+  const bool halves = EPI == kEpiGatedGrad || (EPI == kEpiGated && args.save_h);
+  if (lane == 0) bulk_wait_read_all_but_one();       // the slot's last stores have read it
+  __syncwarp();
+  stage16(slot, args.type, lane, w0);
+  if constexpr (kTwoHalves) {
+    if (halves) {
+      stage16(slot + 1024, args.type, lane, w1);
+      stage16(slot + 2048, args.type, lane, w2);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&P.out16, slot, col, row0);
+    if constexpr (kTwoHalves) {
+      if (halves) {
+        tma_store_3d(&P.out_h16, slot + 1024, col, 0, row0);
+        tma_store_3d(&P.out_h16, slot + 2048, col, 1, row0);
+      }
+    }
+    bulk_commit();
+  }
+}
+
 // The epilogue of a split tile: CTA s of the cluster takes the s-th share of the tile's columns (in
-// steps of 16), adds the CTAs' partial sums from their shared memory in rank order (the result does
-// not depend on timing) and stores directly: few bytes per CTA, and a share may be narrower than a
-// staged row.
+// steps of 16) and adds the CTAs' partial sums from their shared memory in rank order (the result does
+// not depend on timing).
 template <int EPI, int BN>
 __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, int split, int srank,
-                                               uint8_t* parked) {
+                                               uint8_t* parked, uint8_t* buf) {
   constexpr bool I8 = EPI == kEpiInt8;
   constexpr int COLS = EPI == kEpiGated ? BN / 2 : BN;   // output columns of the tile
   int pi, mt, nt;
   dense_tile_at(args, tile, pi, mt, nt);
   const DenseProblem& P = args.p[pi];
   const int rl = (threadIdx.x - 128);                // row of the tile
-  const int row = mt * 128 + rl;
-  if (row >= P.M) return;
+  const int lane = threadIdx.x & 31, row0 = mt * 128 + rl - lane;
+  if (row0 >= P.M) return;                           // (whole warp)
+  const float rs = I8 && row0 + lane < P.M ? args.row_scale[row0 + lane] : 0.f;
+  int n = 0;
   const uint32_t base = smem_addr(parked);
   auto sum16 = [&](int c, float (&v)[16]) {
     int acc[16];
@@ -154,62 +239,34 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
       for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(acc[i]);
     }
   };
-  const int64_t N = P.N;
-  for (int g = srank; g < COLS / 16; g += split) {
-    const int c = 16 * g, col = nt * COLS + c;
-    if (col >= P.N) continue;
-    float v[16];
-    sum16(c, v);
-    if constexpr (EPI == kEpiStore) {
-      store16_cols(P.out_ptr, args.type, N, row, col, v);
-    } else if constexpr (EPI == kEpiInt8) {
-      const float rs = args.row_scale[row];
+  // what the groups read from memory first, in one round of latency (at most half of the groups)
+  constexpr int kMine = COLS / 32;
+  float cl[kMine], bl[kMine];
+  uint4 h[kMine][4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[i] *= rs * __ldg(args.col_scale + col + i);
-        if (args.bias) v[i] += __ldg(args.bias + col + i);
-      }
-      store16_cols(P.out_ptr, args.type, N, row, col, v);
-    } else if constexpr (EPI == kEpiGated) {
-      float u[16], act[16], unused;
-      sum16(COLS + c, u);
+  for (int k = 0; k < kMine; ++k) {
+    const int col = nt * COLS + 16 * (srank + k * split);
+    const bool in = srank + k * split < COLS / 16 && col < P.N;
+    cl[k] = bl[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        gate_fn<false>(args.act, v[i], act[i], unused);
-        act[i] *= u[i];
-      }
-      store16_cols(P.out_ptr, args.type, N, row, col, act);
-      if (args.save_h) {
-        store16_cols(P.out_h_ptr, args.type, 2 * N, row, col, v);
-        store16_cols(P.out_h_ptr, args.type, 2 * N, row, static_cast<int>(N) + col, u);
-      }
-    } else {
-      float act[16], dg[16], du[16];
-      const uint4* hg = reinterpret_cast<const uint4*>(args.h + (int64_t)row * 2 * N + col);
-      const uint4* hu = reinterpret_cast<const uint4*>(args.h + (int64_t)row * 2 * N + N + col);
-      const uint4 gw[2] = {__ldg(hg), __ldg(hg + 1)}, uw[2] = {__ldg(hu), __ldg(hu + 1)};
-      const uint32_t* gp = reinterpret_cast<const uint32_t*>(gw);
-      const uint32_t* up = reinterpret_cast<const uint32_t*>(uw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float g2[2], u2[2];
-        unpack16(args.type, gp[i], g2[0], g2[1]);
-        unpack16(args.type, up[i], u2[0], u2[1]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float f, df;
-          gate_fn<true>(args.act, g2[e], f, df);
-          const int k = 2 * i + e;
-          act[k] = f * u2[e];
-          dg[k] = v[k] * u2[e] * df;
-          du[k] = v[k] * f;
-        }
-      }
-      store16_cols(P.out_ptr, args.type, N, row, col, act);
-      store16_cols(P.out_h_ptr, args.type, 2 * N, row, col, dg);
-      store16_cols(P.out_h_ptr, args.type, 2 * N, row, static_cast<int>(N) + col, du);
+    for (int i = 0; i < 4; ++i) h[k][i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (I8) {
+      if (in) cl[k] = args.col_scale[col + (lane & 15)];
+      if (in && args.bias) bl[k] = args.bias[col + (lane & 15)];
+    } else if constexpr (EPI == kEpiGatedGrad) {
+      if (in && row0 + lane < P.M) load_h16(args.h, P.N, row0 + lane, col, h[k]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int c = 16 * (srank + k * split), col = nt * COLS + c;
+    if (c >= COLS || col >= P.N) break;
+    float v[16], u[16];
+    sum16(c, v);
+    if constexpr (EPI == kEpiGated) sum16(COLS + c, u);
+    finish16<EPI>(args, P, row0, lane, col, rs, cl[k], bl[k], h[k], v, u, buf, n);
+  }
+  if (lane == 0) bulk_wait_all();
 }
 
 template <int EPI, bool PAIR, int BN, bool SPLIT>
@@ -238,6 +295,9 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
   const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x) / split;
   const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x) / split;
   const int total_tiles = args.total_tiles;
+  // columns of a tile: BN, or fewer (a multiple of 16) where that deals them out more evenly
+  const int bn = (PAIR || SPLIT) ? BN : args.bn;
+  const int nb_rows = PAIR ? BN / 2 : bn;            // rows of B staged by one CTA
   if (unit >= total_tiles) return;                  // (both CTAs of a pair together)
 
   // the first kernel of a call clears the status word (the first block starts no later than any
@@ -298,11 +358,15 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         dense_tile_at(args, tile, pi, mt, nt);
         const DenseProblem& P = args.p[pi];
         const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128;
-        const int n0 = nt * BN + static_cast<int>(crank) * C::NB;
+        const int n0 = nt * bn + static_cast<int>(crank) * C::NB;
         const int a_mn = P.a_mn, b_mn = P.b_mn;
         const int kb0 = SPLIT ? P.num_kb * srank / split : 0;
         const int kb1 = SPLIT ? P.num_kb * (srank + 1) / split : P.num_kb;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        // One m-tile: every unit reads its own weight rows once, and units that walked K in step would
+        // ask for the same few columns of a power-of-two pitch at a time; each starts elsewhere.
+        const int turn = !PAIR && args.direct ? (unit * 5) % (kb1 - kb0) : 0;
+        for (int it = kb0; it < kb1; ++it) {
+          const int kb = it + turn < kb1 ? it + turn : it + turn - (kb1 - kb0);
           const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
                                 : mbar_wait(&empty[stage], phase ^ 1u);
           if (!got) {
@@ -312,7 +376,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           }
           uint8_t* sa = stages + stage * C::STAGE_BYTES;
           uint8_t* sb = sa + C::A_BYTES;
-          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (P.a_rows * 128 + C::B_BYTES));
+          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (P.a_rows + nb_rows) * 128);
           if (!C::I8 && a_mn) {
             load2(sa, &P.a, stage, m0, kb * 64, pol);
             load2(sa + 8192, &P.a, stage, m0 + 64, kb * 64, pol);
@@ -323,8 +387,8 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
             if constexpr (PAIR) {
               load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), static_cast<int>(crank), pol);
             } else {
-              load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), 0, pol);
-              load3(sb + C::B_BYTES / 2, &P.b, stage, kb * C::KE, nt * (BN / 2), 1, pol);
+              load3(sb, &P.b, stage, kb * C::KE, nt * (bn / 2), 0, pol);
+              load3(sb + bn * 64, &P.b, stage, kb * C::KE, nt * (bn / 2), 1, pol);
             }
           } else if (!C::I8 && b_mn) {
 #pragma unroll
@@ -370,8 +434,8 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         const int kb0 = SPLIT ? args.p[pi].num_kb * srank / split : 0;
         const int kb1 = SPLIT ? args.p[pi].num_kb * (srank + 1) / split : args.p[pi].num_kb;
         const uint32_t idesc =
-            C::I8 ? idesc_s8_s32(PAIR ? 256 : 128, BN)
-                  : idesc_f16_f32(args.type == kBf16, PAIR ? 256 : 128, BN, a_mn, b_mn);
+            C::I8 ? idesc_s8_s32(PAIR ? 256 : 128, bn)
+                  : idesc_f16_f32(args.type == kBf16, PAIR ? 256 : 128, bn, a_mn, b_mn);
         const int buf = t & 1;
         const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
         const bool freed = PAIR ? mbar_wait_cluster(&tempty[buf], tph ^ 1u)
@@ -444,7 +508,29 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       const int row = row0 + lane;
       const bool rows_any = row0 < P.M;              // this warp has a valid row
       float rs = 0.f;
-      if constexpr (EPI == kEpiInt8) rs = row < P.M ? args.row_scale[row] : 0.f;
+      // Everything the epilogue reads from memory is asked for before the accumulators are waited for:
+      // this lane's row scale, and the scale and bias of column 32 u + lane of every chunk u (a shuffle
+      // hands them out later). Loaded where they are used, they cost a miss per 32 columns: 6.5 us of
+      // a 33 us launch at T = 64, N = 28672.
+      constexpr int kChunks = EPI == kEpiInt8 ? BN / 32 : 1;
+      float cs[kChunks], cb[kChunks];
+      if constexpr (EPI == kEpiInt8) {
+        rs = row < P.M ? args.row_scale[row] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u) {
+          const int col = nt * bn + 32 * u + lane;
+          const bool in = 32 * u + lane < bn && col < P.N;
+          cs[u] = in ? args.col_scale[col] : 0.f;
+          cb[u] = in && args.bias ? args.bias[col] : 0.f;
+        }
+      }
+      auto pick = [&](const float (&v)[kChunks], int u) {
+        float x = v[0];
+#pragma unroll
+        for (int i = 1; i < kChunks; ++i)
+          if (i == u) x = v[i];
+        return x;
+      };
       const bool ok = PAIR ? mbar_wait_cluster(&tfull[buf], tph) : mbar_wait(&tfull[buf], tph);
       bad = __any_sync(0xffffffffu, !ok);
       if (bad) {
@@ -482,7 +568,29 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           bulk_commit();
         }
       };
-      if (rows_any) {
+      if (!PAIR && !SPLIT && args.direct) {
+        // One m-tile: a tile may be any multiple of 16 columns wide, and so are its stores.
+        const int cols = kGatedCols ? bn / 2 : bn;
+#pragma unroll 1
+        for (int c = 0; rows_any && c < cols; c += 16) {
+          const int col = nt * cols + c;
+          if (col >= P.N) break;
+          uint32_t r[16], r2[16];
+          tmem_ld16(tbase + c, r);
+          if constexpr (kGatedCols) tmem_ld16(tbase + cols + c, r2);
+          tmem_wait_ld();
+          float v[16], u[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = C::I8 ? __int2float_rn(static_cast<int>(r[i])) : __uint_as_float(r[i]);
+            if constexpr (kGatedCols) u[i] = __uint_as_float(r2[i]);
+          }
+          const uint4 no_h[4] = {};                  // (kEpiGatedGrad is never direct)
+          const float cl = EPI == kEpiInt8 ? __shfl_sync(0xffffffffu, pick(cs, c / 32), (c & 16) + (lane & 15)) : 0.f;
+          const float bl = EPI == kEpiInt8 ? __shfl_sync(0xffffffffu, pick(cb, c / 32), (c & 16) + (lane & 15)) : 0.f;
+          finish16<EPI>(args, P, row0, lane, col, rs, cl, bl, no_h, v, u, mybuf, nb);
+        }
+      } else if (rows_any) {
         if constexpr (EPI == kEpiStore || EPI == kEpiInt8) {
           // one 128-byte row of staging per chunk: 64 columns of 16 bits, or 32 of fp32
           const bool wide = EPI == kEpiInt8 && args.type == kFp32;
@@ -494,27 +602,14 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
             load32(c, r);
             float v[32];
             if constexpr (EPI == kEpiInt8) {
-              const bool whole = col + 32 <= P.N;    // (N is a multiple of 16)
-              float sc[32];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 s4 = (whole || i < 4)
-                                      ? __ldg(reinterpret_cast<const float4*>(args.col_scale + col) + i)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                sc[4 * i] = s4.x; sc[4 * i + 1] = s4.y; sc[4 * i + 2] = s4.z; sc[4 * i + 3] = s4.w;
-              }
+              const float cl = pick(cs, c / 32), bl = pick(cb, c / 32);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                v[i] = __int2float_rn(static_cast<int>(r[i])) * (rs * sc[i]);
+                v[i] = __int2float_rn(static_cast<int>(r[i])) * (rs * __shfl_sync(0xffffffffu, cl, i));
               if (args.bias) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  if (whole || i < 4) {
-                    const float4 b4 = __ldg(reinterpret_cast<const float4*>(args.bias + col) + i);
-                    v[4 * i] += b4.x; v[4 * i + 1] += b4.y; v[4 * i + 2] += b4.z; v[4 * i + 3] += b4.w;
-                  }
-                }
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bl, i);
               }
             } else {
               tmem_wait_ld();
@@ -549,6 +644,18 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           // Gated epilogues: chunks of 64 features; staging buffer 0 act, 1 gate, 2 up.
           constexpr int HB = EPI == kEpiGated ? BN / 2 : BN;
           const bool halves = EPI == kEpiGatedGrad || args.save_h;
+          // h of the next 32 features is on its way while 32 are worked on
+          uint4 hn[2][4];
+          auto load_h = [&](int c) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) hn[s][i] = make_uint4(0u, 0u, 0u, 0u);
+              const int f = nt * HB + c + 16 * s;
+              if (row < P.M && c + 16 * s < HB && f < P.N) load_h16(args.h, P.N, row, f, hn[s]);
+            }
+          };
+          if constexpr (EPI == kEpiGatedGrad) load_h(0);
 #pragma unroll 1
           for (int c = 0; c < HB; c += 64) {
             const int f0 = nt * HB + c;
@@ -579,15 +686,9 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
                   wu[i] = pack16(args.type, uf[0], uf[1]);
                 }
               } else {
-                uint4 hg[4], hu[4];
-                const uint16_t* hp = args.h + (size_t)row * 2 * P.N + f0 + 32 * half;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const bool in = row < P.M && f0 + 32 * half + 8 * i < P.N;
-                  hg[i] = in ? __ldg(reinterpret_cast<const uint4*>(hp) + i) : make_uint4(0, 0, 0, 0);
-                  hu[i] = in ? __ldg(reinterpret_cast<const uint4*>(hp + P.N) + i)
-                             : make_uint4(0, 0, 0, 0);
-                }
+                const uint4 hg[4] = {hn[0][0], hn[0][1], hn[1][0], hn[1][1]};
+                const uint4 hu[4] = {hn[0][2], hn[0][3], hn[1][2], hn[1][3]};
+                load_h(cc + 32);
                 uint32_t da[32];
                 load32(cc, da);
                 tmem_wait_ld();
@@ -644,7 +745,8 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
   if constexpr (SPLIT) {
     // Every thread of the cluster passes both barriers, also after a timeout.
     cluster_sync_all();                              // all partial sums are parked
-    if (warp >= 4) split_epilogue<EPI, BN>(args, unit, split, srank, stages);
+    if (warp >= 4)
+      split_epilogue<EPI, BN>(args, unit, split, srank, stages, staging + (warp & 3) * C::BUFS * 4096);
   }
   tc_fence_before_sync();
   if constexpr (PAIR || SPLIT) cluster_sync_all();   // (no CTA leaves while another reads its sums)
@@ -671,6 +773,7 @@ DenseTile dense_tile(int epi, const int (*mnk)[3], int n) {
   double best_cost = 0.0;
   auto consider = [&](bool pair, int bn, int split) {
     const int units = pair ? kPlanSMs / 2 : kPlanSMs / split;
+    if (bn > 256 || bn < (epi == kEpiGated ? 32 : 16)) return;
     const int bm = pair ? 256 : 128, cols = epi == kEpiGated ? bn / 2 : bn;
     int64_t tiles = 0, work = 0, longest = 0, rows = 0;
     for (int i = 0; i < n; ++i) {
@@ -692,7 +795,8 @@ DenseTile dense_tile(int epi, const int (*mnk)[3], int n) {
     const double cost = kbs * kb_cost + 10.0 * bn + (split > 1 ? 1500.0 + 300.0 * split : 0.0);
     if (best_cost == 0.0 || cost < best_cost * (1.0 - 1e-9)) {
       best_cost = cost;
-      best = DenseTile{pair, bn, split};
+      best = DenseTile{pair, bn, split,
+                       n == 1 && !pair && split == 1 && mnk[0][0] <= 128 && epi != kEpiGatedGrad};
     }
   };
   consider(true, 256, 1);
@@ -700,6 +804,11 @@ DenseTile dense_tile(int epi, const int (*mnk)[3], int n) {
     consider(false, bn, 1);
     if (n == 1 && bn <= 128)
       for (int split = 2; split <= 8; split *= 2) consider(false, bn, split);
+  }
+  // one m-tile with K-major weights: any width in steps of 16, so that w waves deal the columns out
+  if (n == 1 && mnk[0][0] <= 128 && epi != kEpiGatedGrad) {
+    const int groups = (mnk[0][1] + 15) / 16, each = epi == kEpiGated ? 32 : 16;
+    for (int w = 1; w <= 16; ++w) consider(false, each * ((groups + w * kPlanSMs - 1) / (w * kPlanSMs)), 1);
   }
   return best;
 }
@@ -729,7 +838,7 @@ bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int 
   return make_map(m, w13, 3, dims, str, box, map_type(type));
 }
 
-bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
+static bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
   const int bytes = type == kFp32 ? 4 : 2;
   const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M};
   const uint64_t str[1] = {(uint64_t)N * bytes};
@@ -737,11 +846,27 @@ bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int t
   return make_map(m, base, 2, dims, str, box, map_type(type));
 }
 
-bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type) {
+static bool dense_map_out16(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
+  const int bytes = type == kFp32 ? 4 : 2;
+  const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M};
+  const uint64_t str[1] = {(uint64_t)N * bytes};
+  const uint32_t box[2] = {16, 32};
+  return make_map(m, base, 2, dims, str, box, map_type(type), CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+static bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, int64_t F, int type,
+                          int cols) {
   const uint64_t dims[3] = {(uint64_t)F, 2, (uint64_t)M};
   const uint64_t str[2] = {(uint64_t)F * 2, (uint64_t)F * 4};
-  const uint32_t box[3] = {64, 1, 32};
-  return make_map(m, base, 3, dims, str, box, map_type(type));
+  const uint32_t box[3] = {(uint32_t)cols, 1, 32};
+  return make_map(m, base, 3, dims, str, box, map_type(type),
+                  cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, void* halves) {
+  return dense_map_out(&p->out, out, M, N, type) && dense_map_out16(&p->out16, out, M, N, type) &&
+         (!halves || (dense_map_out_halves(&p->out_h, halves, M, N, type, 64) &&
+                      dense_map_out_halves(&p->out_h16, halves, M, N, type, 16)));
 }
 
 namespace {
@@ -793,19 +918,20 @@ cudaError_t launch_dense_e(DenseTile tile, const DenseArgs& args, cudaStream_t s
     if constexpr (EPI != kEpiGated) return launch_dense_t<EPI, false, 64, true>(args, s);
     return cudaErrorInvalidValue;
   }
-  switch (tile.bn) {
-    case 256: return launch_dense_t<EPI, false, 256, false>(args, s);
-    case 128: return launch_dense_t<EPI, false, 128, false>(args, s);
-    default:
-      if constexpr (EPI != kEpiGated) return launch_dense_t<EPI, false, 64, false>(args, s);
-      return cudaErrorInvalidValue;
-  }
+  if (tile.bn > 128) return launch_dense_t<EPI, false, 256, false>(args, s);
+  if (EPI == kEpiGated || tile.bn > 64) return launch_dense_t<EPI, false, 128, false>(args, s);
+  if constexpr (EPI != kEpiGated) return launch_dense_t<EPI, false, 64, false>(args, s);
+  return cudaErrorInvalidValue;
 }
 }  // namespace
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s) {
   const int bm = tile.pair ? 256 : 128, cols = epi == kEpiGated ? tile.bn / 2 : tile.bn;
   args.split = tile.split;
+  args.bn = tile.bn;
+  args.direct = tile.direct;
+  if (!args.direct && !tile.pair && tile.bn != 64 && tile.bn != 128 && tile.bn != 256)
+    return cudaErrorInvalidValue;
   int64_t total = 0;
   for (int i = 0; i < args.n_problems; ++i) {
     DenseProblem& p = args.p[i];

@@ -198,6 +198,14 @@ __global__ void __launch_bounds__(256, 1) few_rows_kernel(const FewRowsArgs a) {
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[m][j][i] = 0u;
+    float cs = 0.f, cb = 0.f;                         // this thread's output column, fetched early
+    if constexpr (I8) {
+      const int n = sh.first + t * sh.per + (tid & 15);
+      if (n < a.N) {
+        cs = a.col_scale[n];
+        if (a.bias) cb = a.bias[n];
+      }
+    }
     for (int p = first_turn(t); p < turns; p += kFewWarps) {
       load_turn();
       cp_async_wait<C::SLOTS - 1>();                  // this turn's pieces have landed
@@ -264,8 +272,8 @@ __global__ void __launch_bounds__(256, 1) few_rows_kernel(const FewRowsArgs a) {
           store_as(a.h, a.type, (size_t)tok * 2 * a.N + a.N + n, uv);
         }
       } else if constexpr (I8) {
-        float v = __int2float_rn(sum(row, tok)) * (s_scale[tok] * a.col_scale[n]);
-        if (a.bias) v += a.bias[n];
+        float v = __int2float_rn(sum(row, tok)) * (s_scale[tok] * cs);
+        if (a.bias) v += cb;
         store_as(a.out, a.type, at, v);
       } else {
         store_as(a.out, a.type, at, sum(row, tok));

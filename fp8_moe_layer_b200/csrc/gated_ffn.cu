@@ -111,15 +111,12 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   a.save_h = h != nullptr;
   a.status = status;
   DenseProblem& g = a.p[0];
-  g.out_ptr = act;
-  g.out_h_ptr = h;
   g.M = T;
   g.N = F;
   g.K = d;
   if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile) ||
       !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
-      !dense_map_out(&g.out, act, T, F, type) ||
-      !dense_map_out_halves(&g.out_h, h ? h : act, T, h ? F : F / 2, type))
+      !dense_map_outputs(&g, act, T, F, type, h))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -129,13 +126,12 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   b.type = type;
   b.status = status;
   DenseProblem& o = b.p[0];
-  o.out_ptr = y;
   o.M = T;
   o.N = d;
   o.K = F;
   if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile) ||
       !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile) ||
-      !dense_map_out(&o.out, y, T, d, type))
+      !dense_map_outputs(&o, y, T, d, type, nullptr))
     return MOE_ERR_UNSUPPORTED;
   return launch_dense(kEpiStore, tile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -181,15 +177,13 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   a.status = status;
   a.clear_status = 1;
   DenseProblem& g = a.p[0];                        // dL/da = dy W2: W2 [d, F] as it lies
-  g.out_ptr = act;
-  g.out_h_ptr = dh;
   g.M = T;
   g.N = F;
   g.K = d;
   g.b_mn = 1;
   if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile) ||
       !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile) ||
-      !dense_map_out(&g.out, act, T, F, type) || !dense_map_out_halves(&g.out_h, dh, T, F, type))
+      !dense_map_outputs(&g, act, T, F, type, dh))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -221,12 +215,11 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
     o.M = pr.M;
     o.N = pr.N;
     o.K = pr.K;
-    o.out_ptr = pr.out;
     o.a_mn = pr.a_mn;
     o.b_mn = 1;
     if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, wtile) ||
         !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, wtile) ||
-        !dense_map_out(&o.out, pr.out, pr.M, pr.N, type))
+        !dense_map_outputs(&o, pr.out, pr.M, pr.N, type, nullptr))
       return MOE_ERR_UNSUPPORTED;
   }
   return launch_dense(kEpiStore, wtile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -8,7 +8,6 @@ streams); bf16 tensors are passed as their bit patterns and e4m3 tensors as uint
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -142,8 +141,13 @@ def alloc_workspace(dm: MoEDims, device=None) -> torch.Tensor:
     return ws
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(device=None) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream's handle (without building a torch Stream object around it)."""
+    index = None if device is None else torch.device(device).index
+    return _raw_stream(torch.cuda.current_device() if index is None else index)
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -244,25 +248,28 @@ def moe_grouped_ffn_int8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets, p
     T, d = hidden.shape
     E, F, dev = w13.shape[0], w2.shape[2], hidden.device
     dm = dims(T, d, E, F, k_max)
-    with _on(dev):
-        args = [_arg("hidden", hidden, torch.bfloat16, (T, d), dev),
-                _arg("w13", w13, torch.int8, (E, 2 * F, d), dev),
-                _arg("w13_scale", w13_scale, torch.float32, (E, 2 * F), dev),
-                _arg("w2", w2, torch.int8, (E, d, F), dev),
-                _arg("w2_scale", w2_scale, torch.float32, (E, d), dev),
-                _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev)]
-        if perm_token.dtype != torch.int32 or perm_token.device != dev:
-            raise TypeError(f"perm_token must be int32 on {dev}")
-        if perm_token.numel() < T * k_max or not perm_token.is_contiguous():
-            raise ValueError("perm_token must be contiguous and hold T * k_max rows")
-        ws = alloc_workspace(dm, dev) if ws is None else ws
-        out = torch.empty(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
-        if T == 0:
-            out.zero_()
-        xs = torch.empty(T, dtype=torch.float32, device=dev) if want_act_scale else None
-        _check(LIB.moe_grouped_ffn_int8(ctypes.byref(dm), *args, perm_token.data_ptr(),
-                                        out.data_ptr(), _p(xs), _p(ws), ws.numel(),
-                                        _stream(dev)), "moe_grouped_ffn_int8")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return moe_grouped_ffn_int8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets,
+                                        perm_token, k_max, ws, want_act_scale)
+    args = [_arg("hidden", hidden, torch.bfloat16, (T, d), dev),
+            _arg("w13", w13, torch.int8, (E, 2 * F, d), dev),
+            _arg("w13_scale", w13_scale, torch.float32, (E, 2 * F), dev),
+            _arg("w2", w2, torch.int8, (E, d, F), dev),
+            _arg("w2_scale", w2_scale, torch.float32, (E, d), dev),
+            _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,), dev)]
+    if perm_token.dtype != torch.int32 or perm_token.device != dev:
+        raise TypeError(f"perm_token must be int32 on {dev}")
+    if perm_token.numel() < T * k_max or not perm_token.is_contiguous():
+        raise ValueError("perm_token must be contiguous and hold T * k_max rows")
+    ws = alloc_workspace(dm, dev) if ws is None else ws
+    out = torch.empty(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
+    if T == 0:
+        out.zero_()
+    xs = torch.empty(T, dtype=torch.float32, device=dev) if want_act_scale else None
+    _check(LIB.moe_grouped_ffn_int8(ctypes.byref(dm), *args, perm_token.data_ptr(),
+                                    out.data_ptr(), _p(xs), _p(ws), ws.numel(),
+                                    _raw_stream(dev.index)), "moe_grouped_ffn_int8")
     return (out, xs) if want_act_scale else out
 
 
@@ -358,29 +365,28 @@ def moe_forward(hidden, router_w, router_bias, k, k_per_token, w13, w13_scale, w
 
 
 # ------------------------------------------------------------------ int8 and 16-bit operators
-def _on(device: torch.device):
-    """The library launches on the current device: make it the tensors' device for one call."""
+def _elsewhere(device: torch.device) -> bool:
+    """Whether the tensors' device is not the current one. The library launches on the current
+    device, so the caller then makes theirs current and calls again."""
     if device.type != "cuda":
         raise ValueError("tensor must be on a CUDA device")
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return device.index != torch.cuda.current_device()
 
 
 def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     """Pointer of a contiguous, 16-byte aligned tensor of this dtype, shape and device."""
+    p = t.data_ptr()
+    if (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()
+            and not p & 15):
+        return p
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    p = t.data_ptr()
-    if p & 15:
-        raise ValueError(f"{name} must be 16-byte aligned")
-    return p
+    raise ValueError(f"{name} must be contiguous" if not t.is_contiguous()
+                     else f"{name} must be 16-byte aligned")
 
 
 def _workspace(ws: Optional[torch.Tensor], need: int, where: str, device) -> torch.Tensor:
@@ -402,12 +408,14 @@ def moe_quant_int8(x):
     if x.dim() < 1:
         raise ValueError("x must have a last dimension")
     K, dev = x.shape[-1], x.device
-    with _on(dev):
-        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        _check(LIB.moe_quant_int8(scale.numel(), K, DTYPES[x.dtype],
-                                  _arg("x", x, x.dtype, x.shape, dev), codes.data_ptr(),
-                                  scale.data_ptr(), _stream(dev)), "moe_quant_int8")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return moe_quant_int8(x)
+    codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _check(LIB.moe_quant_int8(scale.numel(), K, DTYPES[x.dtype],
+                              _arg("x", x, x.dtype, x.shape, dev), codes.data_ptr(),
+                              scale.data_ptr(), _raw_stream(dev.index)), "moe_quant_int8")
     return codes, scale
 
 
@@ -429,18 +437,20 @@ def moe_matmul_int8(x, w, w_scale, bias=None, x_scale=None, out_dtype=None, ws=N
     out_dtype = out_dtype or (torch.bfloat16 if codes else x.dtype)
     if out_dtype not in DTYPES:
         raise TypeError("out_dtype must be bf16, fp16 or fp32")
-    with _on(dev):
-        xp = _arg("x", x, x.dtype, x.shape, dev)
-        wp = _arg("w", w, torch.int8, (N, K), dev)
-        sp = _arg("w_scale", w_scale, torch.float32, (N,), dev)
-        bp = None if bias is None else _arg("bias", bias, torch.float32, (N,), dev)
-        xs = _arg("x_scale", x_scale, torch.float32, (T,), dev) if codes else None
-        ws = _workspace(ws, LIB.moe_matmul_int8_workspace_bytes(T, N, K), "moe_matmul_int8", dev)
-        out = torch.empty(T, N, dtype=out_dtype, device=dev)
-        _check(LIB.moe_matmul_int8(T, N, K, DTYPES.get(x.dtype, 0), None if codes else xp,
-                                   xp if codes else None, xs, wp, sp, bp, DTYPES[out_dtype],
-                                   out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
-               "moe_matmul_int8")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return moe_matmul_int8(x, w, w_scale, bias, x_scale, out_dtype, ws)
+    xp = _arg("x", x, x.dtype, x.shape, dev)
+    wp = _arg("w", w, torch.int8, (N, K), dev)
+    sp = _arg("w_scale", w_scale, torch.float32, (N,), dev)
+    bp = None if bias is None else _arg("bias", bias, torch.float32, (N,), dev)
+    xs = _arg("x_scale", x_scale, torch.float32, (T,), dev) if codes else None
+    ws = _workspace(ws, LIB.moe_matmul_int8_workspace_bytes(T, N, K), "moe_matmul_int8", dev)
+    out = torch.empty(T, N, dtype=out_dtype, device=dev)
+    _check(LIB.moe_matmul_int8(T, N, K, DTYPES.get(x.dtype, 0), None if codes else xp,
+                               xp if codes else None, xs, wp, sp, bp, DTYPES[out_dtype],
+                               out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev.index)),
+           "moe_matmul_int8")
     return out
 
 
@@ -460,16 +470,18 @@ def moe_gated_ffn(x, w13, w2, activation="silu", save_h=False, ws=None):
     ``save_h`` also h [T, 2F], the pre-activations that the backward pass takes."""
     dm = _ffn_dims(x, w13, w2, activation)
     T, d, F, dev, dt = dm.T, dm.d, dm.F, x.device, x.dtype
-    with _on(dev):
-        xp, w13p = _arg("x", x, dt, (T, d), dev), _arg("w13", w13, dt, (2 * F, d), dev)
-        w2p = _arg("w2", w2, dt, (d, F), dev)
-        ws = _workspace(ws, LIB.moe_gated_ffn_workspace_bytes(ctypes.byref(dm)), "moe_gated_ffn",
-                        dev)
-        y = torch.empty(T, d, dtype=dt, device=dev)
-        h = torch.empty(T, 2 * F, dtype=dt, device=dev) if save_h else None
-        _check(LIB.moe_gated_ffn(ctypes.byref(dm), xp, w13p, w2p, y.data_ptr(),
-                                 h.data_ptr() if save_h else None, ws.data_ptr(), ws.numel(),
-                                 _stream(dev)), "moe_gated_ffn")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return moe_gated_ffn(x, w13, w2, activation, save_h, ws)
+    xp, w13p = _arg("x", x, dt, (T, d), dev), _arg("w13", w13, dt, (2 * F, d), dev)
+    w2p = _arg("w2", w2, dt, (d, F), dev)
+    ws = _workspace(ws, LIB.moe_gated_ffn_workspace_bytes(ctypes.byref(dm)), "moe_gated_ffn",
+                    dev)
+    y = torch.empty(T, d, dtype=dt, device=dev)
+    h = torch.empty(T, 2 * F, dtype=dt, device=dev) if save_h else None
+    _check(LIB.moe_gated_ffn(ctypes.byref(dm), xp, w13p, w2p, y.data_ptr(),
+                             h.data_ptr() if save_h else None, ws.data_ptr(), ws.numel(),
+                             _raw_stream(dev.index)), "moe_gated_ffn")
     return (y, h) if save_h else y
 
 
@@ -478,18 +490,20 @@ def moe_gated_ffn_backward(dy, x, w13, w2, h, activation="silu", need=(True, Tru
     that the forward call kept. ``need`` says which are wanted; the others come back as None."""
     dm = _ffn_dims(x, w13, w2, activation)
     T, d, F, dev, dt = dm.T, dm.d, dm.F, x.device, x.dtype
-    with _on(dev):
-        dyp, xp = _arg("dy", dy, dt, (T, d), dev), _arg("x", x, dt, (T, d), dev)
-        w13p, w2p = _arg("w13", w13, dt, (2 * F, d), dev), _arg("w2", w2, dt, (d, F), dev)
-        hp = _arg("h", h, dt, (T, 2 * F), dev)
-        ws = _workspace(ws, LIB.moe_gated_ffn_backward_workspace_bytes(ctypes.byref(dm)),
-                        "moe_gated_ffn_backward", dev)
-        grads = tuple(torch.empty(n, dtype=dt, device=dev) if want else None
-                      for n, want in zip(((T, d), (2 * F, d), (d, F)), need))
-        gp = [None if g is None else g.data_ptr() for g in grads]
-        _check(LIB.moe_gated_ffn_backward(ctypes.byref(dm), dyp, xp, w13p, w2p, hp, *gp,
-                                          ws.data_ptr(), ws.numel(), _stream(dev)),
-               "moe_gated_ffn_backward")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return moe_gated_ffn_backward(dy, x, w13, w2, h, activation, need, ws)
+    dyp, xp = _arg("dy", dy, dt, (T, d), dev), _arg("x", x, dt, (T, d), dev)
+    w13p, w2p = _arg("w13", w13, dt, (2 * F, d), dev), _arg("w2", w2, dt, (d, F), dev)
+    hp = _arg("h", h, dt, (T, 2 * F), dev)
+    ws = _workspace(ws, LIB.moe_gated_ffn_backward_workspace_bytes(ctypes.byref(dm)),
+                    "moe_gated_ffn_backward", dev)
+    grads = tuple(torch.empty(n, dtype=dt, device=dev) if want else None
+                  for n, want in zip(((T, d), (2 * F, d), (d, F)), need))
+    gp = [None if g is None else g.data_ptr() for g in grads]
+    _check(LIB.moe_gated_ffn_backward(ctypes.byref(dm), dyp, xp, w13p, w2p, hp, *gp,
+                                      ws.data_ptr(), ws.numel(), _raw_stream(dev.index)),
+           "moe_gated_ffn_backward")
     return grads
 
 

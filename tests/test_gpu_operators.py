@@ -59,7 +59,7 @@ def test_quant_int8_non_finite_rows(ops):
 
 # ------------------------------------------------------------------------------ int8 product
 MATMUL = [(1, 16, 16), (1, 4096, 1040), (2, 144, 272), (8, 48, 32), (9, 1040, 48), (16, 272, 144),
-          (3, 528, 19504), (17, 2064, 528), (128, 512, 256),
+          (3, 528, 19504), (17, 2064, 528), (128, 512, 256), (77, 272, 19504), (100, 1040, 4912),
           (129, 528, 272), (300, 4112, 1040), (1003, 2064, 1040), (2100, 1024, 4144)]
 
 
