@@ -16,16 +16,15 @@
 
 namespace moe {
 
-// Rows of at most 2048 elements that are many go to a warp each: no
-// block barrier between a row's maximum and its codes, eight independent rows per block.
-constexpr int kWarpKeep = 8;
-
-// A block or a warp per row (the grid steps over the rows).
-template <int TYPE, bool BLOCK>
-__global__ void __launch_bounds__(256) quant_int8_kernel(const void* __restrict__ x, int64_t rows,
-                                                         int K, int8_t* __restrict__ codes,
-                                                         float* __restrict__ scale,
-                                                         int* __restrict__ status) {
+// A block of up to 256 threads per row (the grid steps over the rows), or a warp for many rows of at most
+// 2048 elements: no block barrier between a row's maximum and its codes. (Longer rows kept in one warp's
+// registers lose more to occupancy than they gain: T = 8192, K = 7168 in bf16 95 us, a block per row 31.)
+template <int TYPE, bool BLOCK, int KEEP>
+__global__ void __launch_bounds__(256) quant_int8_kernel(const void* __restrict__ x,
+                                                                      int64_t rows, int K,
+                                                                      int8_t* __restrict__ codes,
+                                                                      float* __restrict__ scale,
+                                                                      int* __restrict__ status) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
   __shared__ uint32_t red[8];
@@ -33,20 +32,31 @@ __global__ void __launch_bounds__(256) quant_int8_kernel(const void* __restrict_
   const int64_t r0 = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   for (int64_t r = r0; r < rows; r += BLOCK ? gridDim.x : gridDim.x * 8) {
     const uint8_t* row = static_cast<const uint8_t*>(x) + (size_t)r * K * (TYPE == kFp32 ? 4 : 2);
-    const float sc = quantise_row<TYPE, BLOCK, BLOCK ? 4 : kWarpKeep>(row, K, codes + (size_t)r * K, red, blockDim.x);
+    const float sc = quantise_row<TYPE, BLOCK, KEEP>(row, K, codes + (size_t)r * K, red, blockDim.x);
     if ((BLOCK ? threadIdx.x : threadIdx.x & 31) == 0) scale[r] = sc;
   }
 }
 
+namespace {
+template <int TYPE>
+void quant_int8(int64_t rows, int K, const void* x, int8_t* codes, float* scale, int* status,
+                cudaStream_t s) {
+  const bool many = rows >= 8LL * num_sms(), warps = many && K <= 2048;
+  const int vecs = many ? 8 : 4;                     // vectors of 8 per thread, registers permitting
+  const int threads =
+      warps ? 256 : std::min(256, std::max(32, ((K / 8 + (many ? vecs : 1) - 1) / (many ? vecs : 1) + 31) / 32 * 32));
+  const int grid = (int)std::min<int64_t>(warps ? (rows + 7) / 8 : rows, 64LL * num_sms());
+  launch_pdl(warps ? quant_int8_kernel<TYPE, false, 8>
+                   : many ? quant_int8_kernel<TYPE, true, 8> : quant_int8_kernel<TYPE, true, 4>,
+             dim3(grid), dim3(threads), 0, s, x, rows, K, codes, scale, status);
+}
+}  // namespace
+
 cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8_t* codes,
                               float* scale, int* status, cudaStream_t s) {
-  const bool warps = rows >= 8LL * num_sms() && K <= 256 * kWarpKeep;
-  const int threads = warps ? 256 : std::min(256, std::max(32, (K / 8 + 31) / 32 * 32));
-  const int grid = (int)std::min<int64_t>(warps ? (rows + 7) / 8 : rows, 32LL * num_sms());
-  auto* kernel = type == kBf16 ? (warps ? quant_int8_kernel<kBf16, false> : quant_int8_kernel<kBf16, true>)
-                 : type == kFp16 ? (warps ? quant_int8_kernel<kFp16, false> : quant_int8_kernel<kFp16, true>)
-                                 : (warps ? quant_int8_kernel<kFp32, false> : quant_int8_kernel<kFp32, true>);
-  launch_pdl(kernel, dim3(grid), dim3(threads), 0, s, x, rows, K, codes, scale, status);
+  if (type == kBf16) quant_int8<kBf16>(rows, K, x, codes, scale, status, s);
+  else if (type == kFp16) quant_int8<kFp16>(rows, K, x, codes, scale, status, s);
+  else quant_int8<kFp32>(rows, K, x, codes, scale, status, s);
   return cudaGetLastError();
 }
 

@@ -35,20 +35,38 @@ struct Raw8 {
       }
     }
   }
+  // Running maximum of |x| as bits, which order like the values with NaN above infinity (16 bits: two
+  // lanes of a word), and its end as the bits of an fp32 number.
   __device__ __forceinline__ uint32_t absmax(uint32_t m) const {
-    float v[8];
-    values(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < (TYPE == kFp32 ? 2 : 1); ++j) {
+      const uint32_t w[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        m = TYPE == kFp32 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    }
     return m;
+  }
+  static __device__ __forceinline__ uint32_t fp32_bits(uint32_t m) {
+    if constexpr (TYPE == kFp32) return m;
+    const uint32_t top = max(m >> 16, m & 0xFFFFu);
+    if constexpr (TYPE == kBf16) return top << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
   }
 };
 
-// Codes of eight values. Eight IEEE divisions cost more than the row's bytes (T = 8192, K = 7168:
-// 65 us with them, HBM 27), so the quotient is first taken as v * inv, inv = 1/s rounded: within
-// 127 * 2^-23 < 2^-16 of fp32(v / s). Adding 1.5 * 2^23 rounds it to an integer, half to even, in the
-// sum's low bits. Where the remainder comes within 2^-13 of a half the two might round apart, and
-// those eight are divided.
+// Codes of eight values: fp32(v / s) rounded to an integer, half to even. Eight IEEE divisions cost more
+// than the row's bytes (T = 8192, K = 7168 in bf16: 65 us with them, HBM 27), so the quotient comes from
+// inv = fp32(1/s):
+//   16-bit inputs: q = v inv, then one correction q + (v - q s) inv with the remainder exact by fma,
+//     which rounds to fp32(v / s) (Markstein's division, IBM J. Res. Dev. 34, 1990; for every bf16 and
+//     fp16 row maximum and value it gives the code of the division). A quotient that is exactly a half
+//     is common here (0.3 to 0.8 % of bf16 values), so a test for nearness would fail in most warps.
+//   fp32 inputs: v * inv is within 127 * 2^-23 < 2^-16 of fp32(v / s); where it comes within 2^-15 of
+//     a half the two might round apart, and those eight are divided.
+// Adding 1.5 * 2^23 rounds to an integer in the sum's low bits. `fast`: the row's scale is far from
+// the ends of the exponent range, so nothing here is subnormal or infinite.
+template <int TYPE>
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float sc, float inv, bool fast) {
   if (fast) {
     constexpr float kMagic = 12582912.f;
@@ -56,11 +74,17 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float sc, float inv
     float worst = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float r = fmaf(v[j], inv, kMagic);
-      worst = fmaxf(worst, fabsf(fmaf(v[j], inv, kMagic - r)));
+      float r;
+      if constexpr (TYPE == kFp32) {
+        r = fmaf(v[j], inv, kMagic);
+        worst = fmaxf(worst, fabsf(fmaf(v[j], inv, kMagic - r)));
+      } else {
+        const float q = v[j] * inv;
+        r = fmaf(fmaf(-q, sc, v[j]), inv, q) + kMagic;
+      }
       t[j] = __float_as_uint(r);
     }
-    if (worst <= 0.5f - 0.0001220703125f) {
+    if (worst <= 0.5f - 0.000030517578125f) {
       const uint32_t p0 = __byte_perm(t[0], t[1], 0x0040), p1 = __byte_perm(t[2], t[3], 0x0040);
       const uint32_t p2 = __byte_perm(t[4], t[5], 0x0040), p3 = __byte_perm(t[6], t[7], 0x0040);
       return make_uint2(__byte_perm(p0, p1, 0x5410), __byte_perm(p2, p3, 0x5410));
@@ -94,7 +118,7 @@ __device__ __forceinline__ float quantise_row(const void* row, int K, int8_t* co
     w.load(row, i);
     am = w.absmax(am);
   }
-  am = __reduce_max_sync(0xffffffffu, am);
+  am = __reduce_max_sync(0xffffffffu, Raw8<TYPE>::fp32_bits(am));
   if constexpr (BLOCK) {
     named_bar_sync(1, nthreads);                 // red[] of the previous row has been read
     if (lane == 0) red[warp] = am;
@@ -103,7 +127,7 @@ __device__ __forceinline__ float quantise_row(const void* row, int K, int8_t* co
   }
   const float sc = am == 0u ? 1.f : __fdiv_rn(__uint_as_float(am), 127.f);
   // (outside this range scale or reciprocal may be subnormal or not finite)
-  const bool fast = am > __float_as_uint(1e-30f) && am < __float_as_uint(1e30f);
+  const bool fast = am > __float_as_uint(1e-20f) && am < __float_as_uint(1e30f);
   const float inv = __frcp_rn(sc);
   uint2* dst = reinterpret_cast<uint2*>(codes);
   float v[8];
@@ -112,14 +136,14 @@ __device__ __forceinline__ float quantise_row(const void* row, int K, int8_t* co
     const int i = tid + c * step;
     if (i < nv) {
       raw[c].values(v);
-      dst[i] = codes8(v, sc, inv, fast);
+      dst[i] = codes8<TYPE>(v, sc, inv, fast);
     }
   }
   for (int i = tid + KEEP * step; i < nv; i += step) {
     Raw8<TYPE> w;
     w.load(row, i);
     w.values(v);
-    dst[i] = codes8(v, sc, inv, fast);
+    dst[i] = codes8<TYPE>(v, sc, inv, fast);
   }
   return sc;
 }

@@ -29,7 +29,7 @@ def rnd(g, *n):
 
 # ------------------------------------------------------------------------------ quantisation
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (257, 2064), (5, 8192), (2, 8208), (7, 20000), (1500, 272),
+@pytest.mark.parametrize("rows,K", [(1, 16), (3, 48), (257, 2064), (5, 8192), (2, 8208), (7, 20000), (1500, 272), (1300, 4112), (1200, 8192), (1250, 3600),
                                     (2000, 2048)])
 def test_quant_int8_bit_exact(ops, rows, K, dtype):
     g = gen(rows * K)
@@ -41,6 +41,42 @@ def test_quant_int8_bit_exact(ops, rows, K, dtype):
     ref, rs = R.quant_int8(x)
     assert torch.equal(codes.double(), ref)
     assert torch.equal(scale.double(), rs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quant_int8_every_16_bit_quotient(ops, dtype):
+    """Every significand of a row's maximum against every value down to 2^-9 of it (below that the
+    code is 0): the codes of 16-bit rows come from a corrected reciprocal, not from a division."""
+    bits = 8 if dtype == "bf16" else 11
+    n = 1 << (bits - 1)
+    sig = torch.arange(n, 2 * n, device="cuda").float()
+    down = 0.5 ** torch.arange(0, 10, device="cuda").float()
+    values = (sig[None, :] * down[:, None]).reshape(-1)                # 10 n values
+    scale = 2.0 ** (3 - bits)
+    for lo in range(0, n, 256):
+        top = sig[lo:lo + 256, None]
+        x = torch.where(values[None, :] <= top, values[None, :], top)
+        x = torch.cat([top.expand(-1, 16), x, -x], dim=1)
+        x = (x * scale).to(DT[dtype])
+        codes, s = ops.moe_quant_int8(x.contiguous())
+        ref, rs = R.quant_int8(x)
+        assert torch.equal(s.double(), rs)
+        assert torch.equal(codes.double(), ref)
+
+
+def test_quant_int8_extreme_scales(ops):
+    """Rows near the ends of the exponent range, and subnormal ones."""
+    g = gen(3)
+    for dt in (torch.bfloat16, torch.float32):
+        e = torch.tensor([-149, -140, -133, -127, -126, -100, -70, -66, -60, 0, 90, 100, 120, 127],
+                         device="cuda", dtype=torch.float64)
+        x = (torch.rand(len(e), 272, generator=g, device="cuda", dtype=torch.float64) * 2 - 1)
+        x = (x * 2.0 ** e[:, None]).to(dt)
+        codes, scale = ops.moe_quant_int8(x)
+        ref, rs = R.quant_int8(x)
+        live = rs > 0                                   # a scale that underflows divides by 0
+        assert torch.equal(scale.double(), rs) and live.sum() >= 12
+        assert torch.equal(codes.double()[live], ref[live])
 
 
 def test_quant_int8_non_finite_rows(ops):
