@@ -17,6 +17,10 @@ constexpr int kEpiGated = 1;      // columns [gate | up]: act(gate) * up, and h 
 constexpr int kEpiGatedGrad = 2;  // D = dL/d(act(g) u): with h, dL/dg, dL/du and act(g) u
 constexpr int kEpiInt8 = 3;       // row scale x column scale x D (+ bias)
 
+// Routed int8 experts (rows of A grouped by expert, each group with its own weights; pairs only):
+constexpr int kEpiRoutedGated = 4;  // act = silu(gate) * up in fp32, and each row's max |act|
+constexpr int kEpiRoutedDown = 5;   // row scale x column scale x D in fp32
+
 // operand and output types (include/moe_ops.h)
 constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2;
 constexpr int kActSilu = 0, kActGeluTanh = 1;
@@ -44,6 +48,12 @@ struct DenseArgs {
   const float *row_scale, *col_scale, *bias;   // kEpiInt8 (bias may be null)
   int* status;
   int clear_status;              // this launch is the first of its call
+  // routed experts: first row of each group [E + 1], prefix of the groups' 256-row tiles [E + 1],
+  // fp32 output [rows, N], |act| maxima as fp32 bits
+  const int32_t *group_offsets, *group_tiles;
+  int E;
+  float* out32;
+  uint32_t* row_amax;
 };
 
 // Tile of a launch: 256 x 256 on a 2-CTA pair, or 128 x bn on one CTA, its K split over `split` CTAs;
@@ -64,7 +74,16 @@ bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K
 // Gated weights [2][F][K].
 bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, DenseTile tile);
 // Output maps of a problem: out [M][N] and, for the gated epilogues, h or dh [M][2][N] (or null).
-bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, void* halves);
+bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, bool gated,
+                       void* halves);
+
+// The routed experts' launches: args.p[0] with N, K and the maps, args.E and the tables set.
+constexpr int kRoutedRows = 256;   // rows of a tile
+bool dense_map_routed_rows(CUtensorMap* m, const void* codes, int64_t rows, int K);
+bool dense_map_routed_w13(CUtensorMap* m, const void* w, int E, int F, int d);
+bool dense_map_routed_w2(CUtensorMap* m, const void* w, int E, int d, int F);
+bool dense_map_routed_out(CUtensorMap* m, const void* out, int64_t rows, int N);
+cudaError_t launch_routed(int epi, DenseArgs& args, cudaStream_t s);
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s);
 

@@ -18,7 +18,7 @@
 // dy W2, dh W13, dh^T x and dy^T a read the forward's tensors as they lie.
 //
 // Pipeline: TMA (128-byte swizzle) into a ring of stages of 128 bytes of K, one thread issuing
-// tcgen05.mma into double-buffered TMEM accumulators, four epilogue warps; persistent grid, every
+// tcgen05.mma into double-buffered TMEM accumulators, eight epilogue warps; persistent grid, every
 // wait bounded. Tiles (chosen by dense_tile):
 //   pair    256 x 256 on a 2-CTA pair (cta_group::2, M = 256): each CTA stages 128 rows of A and
 //           128 of B per K-block (32 KB) for 256 x 256 of product, so a byte of shared memory
@@ -37,25 +37,36 @@
 
 namespace moe {
 
+// Eight epilogue warps, two per quarter of the TMEM lanes, taking a tile's column units in turn. One
+// unit costs a warp about 370 cycles of arithmetic and 620 of waits (async-proxy fence 300, issuing the
+// TMA store 160, its buffer's release 160), measured on fp32 units of 32 columns; with four warps short
+// contractions waited for their epilogue (down projection of the routed experts, F = 768: 180 us).
+constexpr int kEpiWarps = 8;
+constexpr int kDenseThreads = 128 + 32 * kEpiWarps;
+
 template <int EPI, bool PAIR, int BN, bool SPLIT>
 struct DenseCfg {
-  static constexpr bool I8 = EPI == kEpiInt8;
+  static constexpr bool ROUTED = EPI == kEpiRoutedGated || EPI == kEpiRoutedDown;
+  static constexpr bool I8 = EPI == kEpiInt8 || ROUTED;
   static constexpr int NB = PAIR ? BN / 2 : BN;      // rows of B staged by one CTA
   static constexpr int KE = I8 ? 128 : 64;           // elements of K per stage (128 bytes)
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = NB * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // epilogue staging, per warp: 32 rows x 128 bytes per buffer; the gated epilogues write up to
-  // three tensors per column chunk, the others alternate two buffers
-  static constexpr int BUFS = (EPI == kEpiGated || EPI == kEpiGatedGrad) ? 3 : 2;
-  static constexpr int STG_BYTES = 4 * BUFS * 4096;
+  // epilogue staging, per warp: 32 rows x 128 bytes; the gated epilogues, which write up to three
+  // tensors per unit of 32 features, 3 x 32 rows x 64 bytes
+  static constexpr bool TRIPLE = EPI == kEpiGated || EPI == kEpiGatedGrad;
+  static constexpr int WARP_STG = TRIPLE ? 6144 : 4096;
+  static constexpr int STG_BYTES = kEpiWarps * WARP_STG;
   static constexpr int SMEM_MAX = 232448;
-  static constexpr int FIT = (SMEM_MAX - 1024 - STG_BYTES - 256) / STAGE_BYTES;
+  static constexpr int TABLE = ROUTED ? 2 * (kMaxExperts + 2) * 4 : 0;   // group offsets, tile prefix
+  static constexpr int FIT = (SMEM_MAX - 1024 - STG_BYTES - 256 - TABLE) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
-  static constexpr int SMEM = 1024 + STG_BYTES + STAGES * STAGE_BYTES + 256;
+  static constexpr int SMEM = 1024 + STG_BYTES + STAGES * STAGE_BYTES + 256 + TABLE;
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(STAGES >= 3, "pipeline too shallow");
   static_assert(!PAIR || (BN == 256 && !SPLIT), "pair tiles");
+  static_assert(!ROUTED || PAIR, "routed tiles run on pairs");
   static_assert(EPI != kEpiGated || BN >= 128, "a gated tile stages 64 features at a time");
   // a split tile's partial sums wait in the (by then idle) stages
   static_assert(!SPLIT || STAGES * STAGE_BYTES >= 128 * BN * 4, "exchange buffer");
@@ -84,6 +95,14 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, int lane, int piece0,
 #pragma unroll
   for (int i = 0; i < NW / 4; ++i)
     *reinterpret_cast<uint4*>(buf + lane * 128 + (((piece0 + i) ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// The same for rows of 64 bytes (the 64-byte swizzle: piece c of row r at piece c ^ ((r / 2) & 3)).
+__device__ __forceinline__ void stage_row64(uint8_t* buf, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
@@ -133,7 +152,7 @@ __device__ __forceinline__ void finish16(const DenseArgs& args, const DenseProbl
                                          const uint4 (&h)[4], float (&v)[16], const float (&u)[16],
                                          uint8_t* buf, int& n) {
   constexpr bool kTwoHalves = EPI == kEpiGated || EPI == kEpiGatedGrad;
-  uint8_t* slot = buf + (n++ & 1) * (kTwoHalves ? 4096 : 2048);
+  uint8_t* slot = buf + (n++ & 1) * (kTwoHalves ? 3072 : 2048);
   float w0[16], w1[16], w2[16];                      // output, and the two halves of h or dh
   if constexpr (EPI == kEpiStore) {
 #pragma unroll
@@ -207,7 +226,8 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
   int pi, mt, nt;
   dense_tile_at(args, tile, pi, mt, nt);
   const DenseProblem& P = args.p[pi];
-  const int rl = (threadIdx.x - 128);                // row of the tile
+  const int rl = (threadIdx.x - 128) & 127;          // row of the tile
+  const int hf = (threadIdx.x - 128) >> 7;           // the quarter's two warps take groups in turn
   const int lane = threadIdx.x & 31, row0 = mt * 128 + rl - lane;
   if (row0 >= P.M) return;                           // (whole warp)
   const float rs = I8 && row0 + lane < P.M ? args.row_scale[row0 + lane] : 0.f;
@@ -239,14 +259,14 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
       for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(acc[i]);
     }
   };
-  // what the groups read from memory first, in one round of latency (at most half of the groups)
-  constexpr int kMine = COLS / 32;
+  // what the groups read from memory first, in one round of latency (split >= 2, and two warps)
+  constexpr int kMine = COLS < 128 ? 1 : COLS / 64;
   float cl[kMine], bl[kMine];
   uint4 h[kMine][4];
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    const int col = nt * COLS + 16 * (srank + k * split);
-    const bool in = srank + k * split < COLS / 16 && col < P.N;
+    const int g = srank + (2 * k + hf) * split, col = nt * COLS + 16 * g;
+    const bool in = g < COLS / 16 && col < P.N;
     cl[k] = bl[k] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[k][i] = make_uint4(0u, 0u, 0u, 0u);
@@ -259,7 +279,7 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
   }
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    const int c = 16 * (srank + k * split), col = nt * COLS + c;
+    const int c = 16 * (srank + (2 * k + hf) * split), col = nt * COLS + c;
     if (c >= COLS || col >= P.N) break;
     float v[16], u[16];
     sum16(c, v);
@@ -270,11 +290,14 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
 }
 
 template <int EPI, bool PAIR, int BN, bool SPLIT>
-__global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constant__ DenseArgs args) {
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_gemm_kernel(const __grid_constant__ DenseArgs args) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
   using C = DenseCfg<EPI, PAIR, BN, SPLIT>;
-  constexpr bool kGatedCols = EPI == kEpiGated;     // B tile = BN/2 gate rows + BN/2 up rows
+  constexpr bool kRouted = C::ROUTED;
+  // B tile = BN/2 gate rows + BN/2 up rows
+  constexpr bool kGatedCols = EPI == kEpiGated || EPI == kEpiRoutedGated;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* stages = smem;
@@ -294,11 +317,39 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
   const int srank = SPLIT ? static_cast<int>(cluster_rank()) : 0;
   const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x) / split;
   const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x) / split;
-  const int total_tiles = args.total_tiles;
+  const int total_tiles =
+      kRouted ? args.p[0].n_tiles * args.group_tiles[args.E] : args.total_tiles;
   // columns of a tile: BN, or fewer (a multiple of 16) where that deals them out more evenly
   const int bn = (PAIR || SPLIT) ? BN : args.bn;
   const int nb_rows = PAIR ? BN / 2 : bn;            // rows of B staged by one CTA
   if (unit >= total_tiles) return;                  // (both CTAs of a pair together)
+  int* s_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 256);
+  int* s_tiles = s_off + kMaxExperts + 2;
+  if constexpr (kRouted) {                           // (read after the barrier below)
+    for (int i = threadIdx.x; i <= args.E; i += blockDim.x) {
+      s_off[i] = args.group_offsets[i];
+      s_tiles[i] = args.group_tiles[i];
+    }
+  }
+  // tile -> product (routed: expert), m-tile, n-tile. Routed: an expert's tiles are consecutive, its
+  // m-tiles fastest (they share a weight tile).
+  auto tile_at = [&](int tile, int& p, int& m, int& n) {
+    if constexpr (kRouted) {
+      const int v = tile / args.p[0].n_tiles;
+      int lo = 0, hi = args.E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_tiles[mid] <= v) lo = mid;
+        else hi = mid - 1;
+      }
+      p = lo;
+      const int mts = s_tiles[lo + 1] - s_tiles[lo], local = tile - args.p[0].n_tiles * s_tiles[lo];
+      m = local % mts;
+      n = local / mts;
+    } else {
+      dense_tile_at(args, tile, p, m, n);
+    }
+  };
 
   // the first kernel of a call clears the status word (the first block starts no later than any
   // other, and a wait reports about a second after its block began)
@@ -310,7 +361,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], PAIR ? 8 : 4);
+      mbar_init(&tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
     }
     mbar_init(drain, 1);
     fence_mbarrier_init();
@@ -355,9 +406,9 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       bool ok = true;
       for (int tile = unit; ok && tile < total_tiles; tile += nunits) {
         int pi, mt, nt;
-        dense_tile_at(args, tile, pi, mt, nt);
-        const DenseProblem& P = args.p[pi];
-        const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128;
+        tile_at(tile, pi, mt, nt);
+        const DenseProblem& P = args.p[kRouted ? 0 : pi];
+        const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + (kRouted ? s_off[pi] : 0);
         const int n0 = nt * bn + static_cast<int>(crank) * C::NB;
         const int a_mn = P.a_mn, b_mn = P.b_mn;
         const int kb0 = SPLIT ? P.num_kb * srank / split : 0;
@@ -383,7 +434,12 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           } else {
             load2(sa, &P.a, stage, kb * C::KE, m0, pol);
           }
-          if constexpr (kGatedCols) {
+          if constexpr (EPI == kEpiRoutedGated) {
+            tma_load_4d_pair(sb, &P.b, full_l + 8u * stage, kb * C::KE, nt * (BN / 2),
+                             static_cast<int>(crank), pi, pol);
+          } else if constexpr (EPI == kEpiRoutedDown) {
+            load3(sb, &P.b, stage, kb * C::KE, n0, pi, pol);
+          } else if constexpr (kGatedCols) {
             if constexpr (PAIR) {
               load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), static_cast<int>(crank), pol);
             } else {
@@ -429,7 +485,8 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       const uint32_t tfull_p = PAIR ? cluster_addr(tfull, 1) : 0u;
       for (int tile = unit; ok && tile < total_tiles; tile += nunits, ++t) {
         int pi, mt, nt;
-        dense_tile_at(args, tile, pi, mt, nt);
+        tile_at(tile, pi, mt, nt);
+        if constexpr (kRouted) pi = 0;
         const int a_mn = C::I8 ? 0 : args.p[pi].a_mn, b_mn = C::I8 ? 0 : args.p[pi].b_mn;
         const int kb0 = SPLIT ? args.p[pi].num_kb * srank / split : 0;
         const int kb1 = SPLIT ? args.p[pi].num_kb * (srank + 1) / split : args.p[pi].num_kb;
@@ -493,26 +550,28 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
       mbar_wait(drain, 0);
     }
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue (4 warps)
-    const int q = warp & 3;
-    uint8_t* mybuf = staging + q * C::BUFS * 4096;
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, hf = (warp - 4) >> 2;    // TMEM quarter; which of its two warps
+    uint8_t* mybuf = staging + (warp - 4) * C::WARP_STG;
     bool bad = false;
-    int t = 0, nb = 0;          // tiles done; staged stores so far (alternating two buffers)
+    int t = 0, nb = 0;          // tiles done; 16-column units stored so far
     for (int tile = unit; tile < total_tiles && !bad; tile += nunits, ++t) {
       int pi, mt, nt;
-      dense_tile_at(args, tile, pi, mt, nt);
-      const DenseProblem& P = args.p[pi];
+      tile_at(tile, pi, mt, nt);
+      const DenseProblem& P = args.p[kRouted ? 0 : pi];
       const int buf = t & 1;
       const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
-      const int row0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + 32 * q;
+      const int row0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + 32 * q +
+                       (kRouted ? s_off[pi] : 0);
       const int row = row0 + lane;
-      const bool rows_any = row0 < P.M;              // this warp has a valid row
+      const int row_end = kRouted ? s_off[pi + 1] : P.M;
+      const bool rows_any = row0 < row_end;          // this warp has a valid row
       float rs = 0.f;
       // Everything the epilogue reads from memory is asked for before the accumulators are waited for:
       // this lane's row scale, and the scale and bias of column 32 u + lane of every chunk u (a shuffle
       // hands them out later). Loaded where they are used, they cost a miss per 32 columns: 6.5 us of
       // a 33 us launch at T = 64, N = 28672.
-      constexpr int kChunks = EPI == kEpiInt8 ? BN / 32 : 1;
+      constexpr int kChunks = C::I8 ? BN / 32 : 1;
       float cs[kChunks], cb[kChunks];
       if constexpr (EPI == kEpiInt8) {
         rs = row < P.M ? args.row_scale[row] : 0.f;
@@ -522,6 +581,17 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           const bool in = 32 * u + lane < bn && col < P.N;
           cs[u] = in ? args.col_scale[col] : 0.f;
           cb[u] = in && args.bias ? args.bias[col] : 0.f;
+        }
+      }
+      if constexpr (kRouted) {
+        rs = row < row_end ? args.row_scale[row] : 0.f;
+        const int ld = EPI == kEpiRoutedGated ? 2 * P.N : P.N;
+#pragma unroll
+        for (int u = 0; u < kChunks; ++u) {          // gated: the first half gate, then up columns
+          constexpr int kHalf = EPI == kEpiRoutedGated ? BN / 2 : BN;
+          const int col = nt * kHalf + (32 * u) % kHalf + lane;
+          const int up = 32 * u >= kHalf ? P.N : 0;
+          cs[u] = col < P.N ? args.col_scale[(size_t)pi * ld + up + col] : 0.f;
         }
       }
       auto pick = [&](const float (&v)[kChunks], int u) {
@@ -544,7 +614,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         // pieces are consecutive); the reduction follows the cluster barrier below.
         if (rows_any) {
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 16) {
+          for (int c = 16 * hf; c < BN; c += 32) {
             uint32_t r[16];
             tmem_ld16(tbase + c, r);
             tmem_wait_ld();
@@ -572,7 +642,7 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         // One m-tile: a tile may be any multiple of 16 columns wide, and so are its stores.
         const int cols = kGatedCols ? bn / 2 : bn;
 #pragma unroll 1
-        for (int c = 0; rows_any && c < cols; c += 16) {
+        for (int c = 16 * hf; rows_any && c < cols; c += 32) {
           const int col = nt * cols + c;
           if (col >= P.N) break;
           uint32_t r[16], r2[16];
@@ -591,60 +661,111 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
           finish16<EPI>(args, P, row0, lane, col, rs, cl, bl, no_h, v, u, mybuf, nb);
         }
       } else if (rows_any) {
-        if constexpr (EPI == kEpiStore || EPI == kEpiInt8) {
-          // one 128-byte row of staging per chunk: 64 columns of 16 bits, or 32 of fp32
-          const bool wide = EPI == kEpiInt8 && args.type == kFp32;
+        if constexpr (kRouted) {
+          // fp32 outputs in chunks of 32 columns; rows behind the group's end belong to the next one
+          constexpr int COLS = EPI == kEpiRoutedGated ? BN / 2 : BN;
+          const bool whole = row0 + 32 <= row_end;
+          uint32_t amax = 0u;
 #pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {
-            const int col = nt * BN + c;
+          for (int c = 32 * hf; c < COLS; c += 64) {
+            const int col = nt * COLS + c;
             if (col >= P.N) break;
-            uint32_t r[32];
+            uint32_t r[32], w[32];
             load32(c, r);
-            float v[32];
-            if constexpr (EPI == kEpiInt8) {
-              const float cl = pick(cs, c / 32), bl = pick(cb, c / 32);
+            const float cl = pick(cs, c / 32);
+            if constexpr (EPI == kEpiRoutedGated) {
+              uint32_t r2[32];
+              load32(COLS + c, r2);
+              const float cu = pick(cs, (COLS + c) / 32);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float g = __int2float_rn(static_cast<int>(r[i])) * (rs * __shfl_sync(0xffffffffu, cl, i));
+                const float u = __int2float_rn(static_cast<int>(r2[i])) * (rs * __shfl_sync(0xffffffffu, cu, i));
+                w[i] = __float_as_uint(silu(g) * u);
+                amax = max(amax, w[i] & 0x7FFFFFFFu);   // (a NaN counts as the largest)
+              }
+            } else {
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                v[i] = __int2float_rn(static_cast<int>(r[i])) * (rs * __shfl_sync(0xffffffffu, cl, i));
-              if (args.bias) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bl, i);
-              }
-            } else {
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                w[i] = __float_as_uint(__int2float_rn(static_cast<int>(r[i])) *
+                                       (rs * __shfl_sync(0xffffffffu, cl, i)));
             }
-            uint8_t* b = mybuf + (nb & 1) * 4096;
-            const bool first = wide || (c & 32) == 0;
-            if (first) {                             // the store before last has read this buffer
-              if (lane == 0) bulk_wait_read_all_but_one();
-              __syncwarp();
-            }
-            if (wide) {
-              uint32_t w[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+            uint8_t* b = mybuf;
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            if (whole) {
               stage_row(b, lane, 0, w);
               store2(b, &P.out, col);
-              ++nb;
             } else {
-              uint32_t w[16];
+              // ragged: dense staging rows, each valid one an untiled store of its own
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = pack16(args.type, v[2 * i], v[2 * i + 1]);
-              stage_row(b, lane, first ? 0 : 4, w);
-              if (!first || col + 32 >= P.N) {
-                store2(b, &P.out, col - (c & 32));
-                ++nb;
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(b + lane * 128 + 16 * i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (row < row_end)
+                bulk_store(args.out32 + (size_t)row * P.N + col, b + lane * 128,
+                           4 * min(32, P.N - col));
+              bulk_commit();                         // (every lane, in its own groups)
+              bulk_wait_read_all();
+              __syncwarp();
             }
           }
+          if constexpr (EPI == kEpiRoutedGated) {
+            if (row < row_end) atomicMax(&args.row_amax[row], amax);
+          }
+        } else if constexpr (EPI == kEpiStore || EPI == kEpiInt8) {
+          // a unit is a 128-byte row of staging: 64 columns of 16 bits, or 32 of fp32
+          const bool wide = EPI == kEpiInt8 && args.type == kFp32;
+          const int unit_cols = wide ? 32 : 64;
+#pragma unroll 1
+          for (int c0 = unit_cols * hf; c0 < BN; c0 += 2 * unit_cols) {
+            const int col0 = nt * BN + c0;
+            if (col0 >= P.N) break;
+            if (lane == 0) bulk_wait_read_all();     // this warp's last store has read the buffer
+            __syncwarp();
+#pragma unroll 1
+            for (int c = c0; c < c0 + unit_cols && nt * BN + c < P.N; c += 32) {
+              uint32_t r[32];
+              load32(c, r);
+              float v[32];
+              if constexpr (EPI == kEpiInt8) {
+                const float cl = pick(cs, c / 32), bl = pick(cb, c / 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[i] = __int2float_rn(static_cast<int>(r[i])) * (rs * __shfl_sync(0xffffffffu, cl, i));
+                if (args.bias) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bl, i);
+                }
+              } else {
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+              }
+              if (wide) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+                stage_row(mybuf, lane, 0, w);
+              } else {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack16(args.type, v[2 * i], v[2 * i + 1]);
+                stage_row(mybuf, lane, (c - c0) / 8, w);
+              }
+            }
+            store2(mybuf, &P.out, col0);
+          }
         } else {
-          // Gated epilogues: chunks of 64 features; staging buffer 0 act, 1 gate, 2 up.
+          // Gated epilogues: units of 32 features; staging of act, then gate, then up.
           constexpr int HB = EPI == kEpiGated ? BN / 2 : BN;
           const bool halves = EPI == kEpiGatedGrad || args.save_h;
-          // h of the next 32 features is on its way while 32 are worked on
+          // h of the next unit is on its way while one is worked on
           uint4 hn[2][4];
           auto load_h = [&](int c) {
 #pragma unroll
@@ -652,80 +773,76 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
 #pragma unroll
               for (int i = 0; i < 4; ++i) hn[s][i] = make_uint4(0u, 0u, 0u, 0u);
               const int f = nt * HB + c + 16 * s;
-              if (row < P.M && c + 16 * s < HB && f < P.N) load_h16(args.h, P.N, row, f, hn[s]);
+              if (row < P.M && c < HB && f < P.N) load_h16(args.h, P.N, row, f, hn[s]);
             }
           };
-          if constexpr (EPI == kEpiGatedGrad) load_h(0);
+          if constexpr (EPI == kEpiGatedGrad) load_h(32 * hf);
 #pragma unroll 1
-          for (int c = 0; c < HB; c += 64) {
+          for (int c = 32 * hf; c < HB; c += 64) {
             const int f0 = nt * HB + c;
             if (f0 >= P.N) break;
-            if (lane == 0) bulk_wait_read_all();     // the previous chunk's stores have read
+            uint32_t wa[16], wg[16], wu[16];
+            if constexpr (EPI == kEpiGated) {
+              uint32_t g[32], u[32];
+              load32(c, g);
+              load32(HB + c, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float a[2], gf[2], uf[2], unused;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  gf[e] = __uint_as_float(g[2 * i + e]);
+                  uf[e] = __uint_as_float(u[2 * i + e]);
+                  gate_fn<false>(args.act, gf[e], a[e], unused);
+                  a[e] *= uf[e];
+                }
+                wa[i] = pack16(args.type, a[0], a[1]);
+                wg[i] = pack16(args.type, gf[0], gf[1]);
+                wu[i] = pack16(args.type, uf[0], uf[1]);
+              }
+            } else {
+              const uint4 hg[4] = {hn[0][0], hn[0][1], hn[1][0], hn[1][1]};
+              const uint4 hu[4] = {hn[0][2], hn[0][3], hn[1][2], hn[1][3]};
+              load_h(c + 64);
+              uint32_t da[32];
+              load32(c, da);
+              tmem_wait_ld();
+              const uint32_t* hgw = reinterpret_cast<const uint32_t*>(hg);
+              const uint32_t* huw = reinterpret_cast<const uint32_t*>(hu);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float g[2], u[2], a[2], dg[2], du[2];
+                unpack16(args.type, hgw[i], g[0], g[1]);
+                unpack16(args.type, huw[i], u[0], u[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float f, df;
+                  gate_fn<true>(args.act, g[e], f, df);
+                  const float d = __uint_as_float(da[2 * i + e]);
+                  a[e] = f * u[e];
+                  dg[e] = d * u[e] * df;
+                  du[e] = d * f;
+                }
+                wa[i] = pack16(args.type, a[0], a[1]);
+                wg[i] = pack16(args.type, dg[0], dg[1]);
+                wu[i] = pack16(args.type, du[0], du[1]);
+              }
+            }
+            if (lane == 0) bulk_wait_read_all();     // the last unit's stores have read the buffers
             __syncwarp();
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              const int cc = c + 32 * half;
-              uint32_t wa[16], wg[16], wu[16];
-              if constexpr (EPI == kEpiGated) {
-                uint32_t g[32], u[32];
-                load32(cc, g);
-                load32(HB + cc, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float a[2], gf[2], uf[2], unused;
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    gf[e] = __uint_as_float(g[2 * i + e]);
-                    uf[e] = __uint_as_float(u[2 * i + e]);
-                    gate_fn<false>(args.act, gf[e], a[e], unused);
-                    a[e] *= uf[e];
-                  }
-                  wa[i] = pack16(args.type, a[0], a[1]);
-                  wg[i] = pack16(args.type, gf[0], gf[1]);
-                  wu[i] = pack16(args.type, uf[0], uf[1]);
-                }
-              } else {
-                const uint4 hg[4] = {hn[0][0], hn[0][1], hn[1][0], hn[1][1]};
-                const uint4 hu[4] = {hn[0][2], hn[0][3], hn[1][2], hn[1][3]};
-                load_h(cc + 32);
-                uint32_t da[32];
-                load32(cc, da);
-                tmem_wait_ld();
-                const uint32_t* hgw = reinterpret_cast<const uint32_t*>(hg);
-                const uint32_t* huw = reinterpret_cast<const uint32_t*>(hu);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float g[2], u[2], a[2], dg[2], du[2];
-                  unpack16(args.type, hgw[i], g[0], g[1]);
-                  unpack16(args.type, huw[i], u[0], u[1]);
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    float f, df;
-                    gate_fn<true>(args.act, g[e], f, df);
-                    const float d = __uint_as_float(da[2 * i + e]);
-                    a[e] = f * u[e];
-                    dg[e] = d * u[e] * df;
-                    du[e] = d * f;
-                  }
-                  wa[i] = pack16(args.type, a[0], a[1]);
-                  wg[i] = pack16(args.type, dg[0], dg[1]);
-                  wu[i] = pack16(args.type, du[0], du[1]);
-                }
-              }
-              stage_row(mybuf, lane, 4 * half, wa);
-              if (halves) {
-                stage_row(mybuf + 4096, lane, 4 * half, wg);
-                stage_row(mybuf + 8192, lane, 4 * half, wu);
-              }
+            stage_row64(mybuf, lane, wa);
+            if (halves) {
+              stage_row64(mybuf + 2048, lane, wg);
+              stage_row64(mybuf + 4096, lane, wu);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               tma_store_2d(&P.out, mybuf, f0, row0);
               if (halves) {
-                tma_store_3d(&P.out_h, mybuf + 4096, f0, 0, row0);
-                tma_store_3d(&P.out_h, mybuf + 8192, f0, 1, row0);
+                tma_store_3d(&P.out_h, mybuf + 2048, f0, 0, row0);
+                tma_store_3d(&P.out_h, mybuf + 4096, f0, 1, row0);
               }
               bulk_commit();
             }
@@ -739,14 +856,14 @@ __global__ void __launch_bounds__(256, 1) dense_gemm_kernel(const __grid_constan
         else mbar_arrive(&tempty[buf]);
       }
     }
-    if (lane == 0) bulk_wait_all();                  // this warp's stores have completed
+    if (kRouted || lane == 0) bulk_wait_all();       // this warp's stores have completed
   }
 
   if constexpr (SPLIT) {
     // Every thread of the cluster passes both barriers, also after a timeout.
     cluster_sync_all();                              // all partial sums are parked
     if (warp >= 4)
-      split_epilogue<EPI, BN>(args, unit, split, srank, stages, staging + (warp & 3) * C::BUFS * 4096);
+      split_epilogue<EPI, BN>(args, unit, split, srank, stages, staging + (warp - 4) * C::WARP_STG);
   }
   tc_fence_before_sync();
   if constexpr (PAIR || SPLIT) cluster_sync_all();   // (no CTA leaves while another reads its sums)
@@ -838,12 +955,14 @@ bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int 
   return make_map(m, w13, 3, dims, str, box, map_type(type));
 }
 
-static bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
+static bool dense_map_out(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type,
+                          int row_bytes = 128) {
   const int bytes = type == kFp32 ? 4 : 2;
   const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M};
   const uint64_t str[1] = {(uint64_t)N * bytes};
-  const uint32_t box[2] = {(uint32_t)(128 / bytes), 32};
-  return make_map(m, base, 2, dims, str, box, map_type(type));
+  const uint32_t box[2] = {(uint32_t)(row_bytes / bytes), 32};
+  return make_map(m, base, 2, dims, str, box, map_type(type),
+                  row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 static bool dense_map_out16(CUtensorMap* m, const void* base, int64_t M, int64_t N, int type) {
@@ -860,12 +979,13 @@ static bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, in
   const uint64_t str[2] = {(uint64_t)F * 2, (uint64_t)F * 4};
   const uint32_t box[3] = {(uint32_t)cols, 1, 32};
   return make_map(m, base, 3, dims, str, box, map_type(type),
-                  cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+                  cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, void* halves) {
-  return dense_map_out(&p->out, out, M, N, type) && dense_map_out16(&p->out16, out, M, N, type) &&
-         (!halves || (dense_map_out_halves(&p->out_h, halves, M, N, type, 64) &&
+bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, bool gated,
+                       void* halves) {
+  return dense_map_out(&p->out, out, M, N, type, gated ? 64 : 128) && dense_map_out16(&p->out16, out, M, N, type) &&
+         (!halves || (dense_map_out_halves(&p->out_h, halves, M, N, type, 32) &&
                       dense_map_out_halves(&p->out_h16, halves, M, N, type, 16)));
 }
 
@@ -886,7 +1006,7 @@ cudaError_t launch_dense_t(const DenseArgs& args, cudaStream_t s) {
     if (PAIR) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(num_sms());
-      cfg.blockDim = dim3(256);
+      cfg.blockDim = dim3(kDenseThreads);
       cfg.dynamicSmemBytes = C::SMEM;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -905,8 +1025,8 @@ cudaError_t launch_dense_t(const DenseArgs& args, cudaStream_t s) {
   }
   const int units = SPLIT ? args.total_tiles : std::min(unit_cache[dev], args.total_tiles);
   const int cluster = PAIR ? 2 : SPLIT ? args.split : 1;
-  launch_pdl_cluster(dense_gemm_kernel<EPI, PAIR, BN, SPLIT>, dim3(units * cluster), dim3(256), C::SMEM,
-                     cluster, s, args);
+  launch_pdl_cluster(dense_gemm_kernel<EPI, PAIR, BN, SPLIT>, dim3(units * cluster), dim3(kDenseThreads),
+                     C::SMEM, cluster, s, args);
   return cudaGetLastError();
 }
 
@@ -924,6 +1044,42 @@ cudaError_t launch_dense_e(DenseTile tile, const DenseArgs& args, cudaStream_t s
   return cudaErrorInvalidValue;
 }
 }  // namespace
+
+bool dense_map_routed_rows(CUtensorMap* m, const void* codes, int64_t rows, int K) {
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)K};
+  const uint32_t box[2] = {128, 128};
+  return make_map(m, codes, 2, dims, str, box);
+}
+bool dense_map_routed_w13(CUtensorMap* m, const void* w, int E, int F, int d) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)F, 2, (uint64_t)E};
+  const uint64_t str[3] = {(uint64_t)d, (uint64_t)F * d, 2ull * F * d};
+  const uint32_t box[4] = {128, 128, 1, 1};
+  return make_map(m, w, 4, dims, str, box);
+}
+bool dense_map_routed_w2(CUtensorMap* m, const void* w, int E, int d, int F) {
+  const uint64_t dims[3] = {(uint64_t)F, (uint64_t)d, (uint64_t)E};
+  const uint64_t str[2] = {(uint64_t)F, (uint64_t)d * F};
+  const uint32_t box[3] = {128, 128, 1};
+  return make_map(m, w, 3, dims, str, box);
+}
+bool dense_map_routed_out(CUtensorMap* m, const void* out, int64_t rows, int N) {
+  return dense_map_out(m, out, rows, N, kFp32);
+}
+
+cudaError_t launch_routed(int epi, DenseArgs& args, cudaStream_t s) {
+  DenseProblem& p = args.p[0];
+  const int cols = epi == kEpiRoutedGated ? 128 : 256;
+  args.n_problems = 1;
+  args.bn = 256;
+  args.split = 1;
+  p.a_rows = 128;
+  p.n_tiles = (p.N + cols - 1) / cols;
+  p.num_kb = (p.K + 127) / 128;
+  args.total_tiles = 1 << 30;       // (the kernel reads the real count)
+  return epi == kEpiRoutedGated ? launch_dense_t<kEpiRoutedGated, true, 256, false>(args, s)
+                                : launch_dense_t<kEpiRoutedDown, true, 256, false>(args, s);
+}
 
 cudaError_t launch_dense(int epi, DenseTile tile, DenseArgs& args, cudaStream_t s) {
   const int bm = tile.pair ? 256 : 128, cols = epi == kEpiGated ? tile.bn / 2 : tile.bn;

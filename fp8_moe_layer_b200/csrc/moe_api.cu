@@ -445,6 +445,42 @@ static int run_ffn(const Plan& p, const Ws& w, const uint8_t* w13, const float* 
   return MOE_OK;
 }
 
+// Mean rows per expert from which moe_grouped_ffn_int8 uses the routed dense GEMMs.
+constexpr int kRoutedMeanRows = 128;
+
+static int routed_ffn_int8(const Plan& p, const Ws& w, const uint8_t* w13, const float* w13_scale,
+                           const uint8_t* w2, const float* w2_scale, float* expert_out,
+                           cudaStream_t s) {
+  DenseArgs a{};
+  a.E = p.E;
+  a.group_offsets = w.offsets;
+  a.group_tiles = w.tiles;
+  a.row_scale = w.xsp;
+  a.col_scale = w13_scale;
+  a.status = w.status;
+  a.out32 = w.act;
+  a.row_amax = w.amax;
+  a.p[0].N = p.F;
+  a.p[0].K = p.d;
+  if (!dense_map_routed_rows(&a.p[0].a, w.xqp, p.Rpad, p.d) ||
+      !dense_map_routed_w13(&a.p[0].b, w13, p.E, p.F, p.d) ||
+      !dense_map_routed_out(&a.p[0].out, w.act, p.Rpad, p.F))
+    return MOE_ERR_UNSUPPORTED;
+  MOE_CUDA(launch_routed(kEpiRoutedGated, a, s));
+  MOE_CUDA(launch_requant(p, w.act, w.amax, w.offsets + p.E, w.aq, w.s2, s));
+  a.row_scale = w.s2;
+  a.col_scale = w2_scale;
+  a.out32 = expert_out;
+  a.p[0].N = p.d;
+  a.p[0].K = p.F;
+  if (!dense_map_routed_rows(&a.p[0].a, w.aq, p.Rpad, p.F) ||
+      !dense_map_routed_w2(&a.p[0].b, w2, p.E, p.d, p.F) ||
+      !dense_map_routed_out(&a.p[0].out, expert_out, p.Rcap, p.d))
+    return MOE_ERR_UNSUPPORTED;
+  MOE_CUDA(launch_routed(kEpiRoutedDown, a, s));
+  return MOE_OK;
+}
+
 // moe_grouped_ffn_fp8 and moe_grouped_ffn_int8: the same steps on codes of either format.
 static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, const uint8_t* w13,
                        const float* w13_scale, const uint8_t* w2, const float* w2_scale,
@@ -469,7 +505,12 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
   q.Rcap = (int64_t)p.T * p.k_max;
   q.int8 = int8;
   if (int8) {
-    const Int8Prepare pre{hidden, expert_offsets, perm_token, p.T, p.d, p.E, p.BN, q.Rcap, w.tiles,
+    // Prefill-sized groups run on the routed form of the dense GEMM (256-row tiles of tokens on pairs):
+    // its epilogue keeps gate and up of a feature in one thread. Smaller groups would leave such tiles
+    // mostly empty and keep the weights-as-rows kernels.
+    const bool routed = q.Rcap >= (int64_t)kRoutedMeanRows * p.E;
+    const Int8Prepare pre{hidden, expert_offsets, perm_token, p.T, p.d, p.E,
+                          routed ? kRoutedRows : p.BN, q.Rcap, w.tiles,
                           reinterpret_cast<int8_t*>(w.xq), w.xs, reinterpret_cast<int8_t*>(w.xqp), w.xsp, w.amax,
                           expert_out, w.status};
     MOE_CUDA(launch_int8_prepare(pre, s));
@@ -477,6 +518,7 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
       MOE_CUDA(launch_quant_int8(p.T, p.d, kBf16, hidden, reinterpret_cast<int8_t*>(w.xq),
                                  act_scale_out, nullptr, s));
     w.offsets = const_cast<int32_t*>(expert_offsets);      // read only from here on
+    if (routed) return routed_ffn_int8(q, w, w13, w13_scale, w2, w2_scale, expert_out, s);
   } else {
     MOE_CUDA(launch_topk_quant(q, nullptr, nullptr, 1, nullptr, nullptr, nullptr, hidden, w.xq,
                                w.xs, false, true, nullptr, w.status, s));

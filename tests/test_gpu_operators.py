@@ -177,7 +177,8 @@ def test_gated_ffn_backward(ops, T, d, F, dtype, act):
 # (T, d, E, F, k): decode tiles with a K split, ragged groups, experts without a token, prefill
 # tiles of 64 to 256 rows on one CTA and on pairs
 EXPERTS = [(1, 64, 8, 32, 2), (1, 2048, 128, 768, 8), (5, 528, 6, 272, 3), (64, 1024, 16, 528, 4),
-           (300, 528, 4, 336, 2), (700, 272, 3, 2064, 3), (2048, 256, 8, 208, 2)]
+           (300, 528, 4, 336, 2), (700, 272, 3, 2064, 3), (2048, 256, 8, 208, 2),
+           (1500, 528, 7, 336, 3), (2100, 144, 16, 1040, 5)]
 
 
 def routed(T, E, k, g):
