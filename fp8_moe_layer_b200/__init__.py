@@ -2,11 +2,12 @@
 FFN and weighted combine, as hand-written sm_100a CUDA kernels behind a small C ABI.
 
 ``fp8_moe_layer_b200.ops`` is the Python binding of that C ABI (it loads the compiled library
-and raises if it is missing); ``fp8_moe_layer_b200.inputs`` draws seeded synthetic layers.
+and raises if it is missing); ``fp8_moe_layer_b200.inputs`` draws seeded synthetic layers;
+``fp8_moe_layer_b200.gated_ffn`` has the dense gated FFN as torch modules.
 The binding is imported on first use so that the input generator works without a GPU build.
 """
 
-__all__ = ["ops", "inputs"]
+__all__ = ["ops", "inputs", "gated_ffn"]
 
 
 def __getattr__(name):

@@ -73,9 +73,9 @@ bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K
                        int type, bool mn, bool is_a, DenseTile tile);
 // Gated weights [2][F][K].
 bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, DenseTile tile);
-// Output maps of a problem: out [M][N] and, for the gated epilogues, h or dh [M][2][N] (or null).
-bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, bool gated,
-                       void* halves);
+// The output maps that a problem's tile uses: out [M][N] and, for the gated epilogues, h or dh [M][2][N] (or null).
+bool dense_map_outputs(DenseProblem* p, DenseTile tile, void* out, int64_t M, int64_t N, int type,
+                       bool gated, void* halves);
 
 // The routed experts' launches: args.p[0] with N, K and the maps, args.E and the tables set.
 constexpr int kRoutedRows = 256;   // rows of a tile

@@ -982,11 +982,13 @@ static bool dense_map_out_halves(CUtensorMap* m, const void* base, int64_t M, in
                   cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-bool dense_map_outputs(DenseProblem* p, void* out, int64_t M, int64_t N, int type, bool gated,
-                       void* halves) {
-  return dense_map_out(&p->out, out, M, N, type, gated ? 64 : 128) && dense_map_out16(&p->out16, out, M, N, type) &&
-         (!halves || (dense_map_out_halves(&p->out_h, halves, M, N, type, 32) &&
-                      dense_map_out_halves(&p->out_h16, halves, M, N, type, 16)));
+bool dense_map_outputs(DenseProblem* p, DenseTile tile, void* out, int64_t M, int64_t N, int type,
+                       bool gated, void* halves) {
+  if (tile.direct || tile.split > 1)
+    return dense_map_out16(&p->out16, out, M, N, type) &&
+           (!halves || dense_map_out_halves(&p->out_h16, halves, M, N, type, 16));
+  return dense_map_out(&p->out, out, M, N, type, gated ? 64 : 128) &&
+         (!halves || dense_map_out_halves(&p->out_h, halves, M, N, type, 32));
 }
 
 namespace {

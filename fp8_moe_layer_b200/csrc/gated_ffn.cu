@@ -116,7 +116,7 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   g.K = d;
   if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile) ||
       !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
-      !dense_map_outputs(&g, act, T, F, type, true, h))
+      !dense_map_outputs(&g, tile, act, T, F, type, true, h))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -131,7 +131,7 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   o.K = F;
   if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile) ||
       !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile) ||
-      !dense_map_outputs(&o, y, T, d, type, false, nullptr))
+      !dense_map_outputs(&o, tile, y, T, d, type, false, nullptr))
     return MOE_ERR_UNSUPPORTED;
   return launch_dense(kEpiStore, tile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -183,7 +183,7 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   g.b_mn = 1;
   if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile) ||
       !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile) ||
-      !dense_map_outputs(&g, act, T, F, type, true, dh))
+      !dense_map_outputs(&g, tile, act, T, F, type, true, dh))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
@@ -219,7 +219,7 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
     o.b_mn = 1;
     if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, wtile) ||
         !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, wtile) ||
-        !dense_map_outputs(&o, pr.out, pr.M, pr.N, type, false, nullptr))
+        !dense_map_outputs(&o, wtile, pr.out, pr.M, pr.N, type, false, nullptr))
       return MOE_ERR_UNSUPPORTED;
   }
   return launch_dense(kEpiStore, wtile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -250,7 +250,7 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
   DenseProblem& d = a.p[0];
   if (!dense_map_operand(&d.a, codes, T, K, 1, 0, false, true, tile) ||
       !dense_map_operand(&d.b, w, N, K, 1, 0, false, false, tile) ||
-      !dense_map_outputs(&d, out, T, N, out_type, false, nullptr))
+      !dense_map_outputs(&d, tile, out, T, N, out_type, false, nullptr))
     return MOE_ERR_UNSUPPORTED;
   d.M = T;
   d.N = N;

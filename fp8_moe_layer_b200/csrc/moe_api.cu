@@ -445,8 +445,10 @@ static int run_ffn(const Plan& p, const Ws& w, const uint8_t* w13, const float* 
   return MOE_OK;
 }
 
-// Mean rows per expert from which moe_grouped_ffn_int8 uses the routed dense GEMMs.
-constexpr int kRoutedMeanRows = 128;
+// Mean rows per expert from which moe_grouped_ffn_int8 uses the routed dense GEMMs. Whole calls, weights
+// as rows against routed: 128 rows (E 8, d 4096, F 14336) 320 : 359 us, 256 rows 488 : 511; 512 rows (E 32,
+// d 7168, F 2048) 921 : 839; 1024 rows (E 8, d 4096, F 4096) 482 : 464, (E 64, d 2048, F 1024) 786 : 683.
+constexpr int kRoutedMeanRows = 384;
 
 static int routed_ffn_int8(const Plan& p, const Ws& w, const uint8_t* w13, const float* w13_scale,
                            const uint8_t* w2, const float* w2_scale, float* expert_out,
@@ -505,9 +507,9 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
   q.Rcap = (int64_t)p.T * p.k_max;
   q.int8 = int8;
   if (int8) {
-    // Prefill-sized groups run on the routed form of the dense GEMM (256-row tiles of tokens on pairs):
-    // its epilogue keeps gate and up of a feature in one thread. Smaller groups would leave such tiles
-    // mostly empty and keep the weights-as-rows kernels.
+    // Large groups run on the routed form of the dense GEMM (256-row tiles of tokens on pairs, gate and
+    // up of a feature in one thread); smaller ones would leave such tiles part empty and keep the
+    // weights-as-rows kernels, whose tiles take any number of tokens.
     const bool routed = q.Rcap >= (int64_t)kRoutedMeanRows * p.E;
     const Int8Prepare pre{hidden, expert_offsets, perm_token, p.T, p.d, p.E,
                           routed ? kRoutedRows : p.BN, q.Rcap, w.tiles,

@@ -1,0 +1,88 @@
+"""The dense gated FFN as torch modules: 16 bits with gradients while a shared expert or a dense
+layer is trained, W8A8 int8 when it is served.
+
+``gated_ffn`` is differentiable (``ops.moe_gated_ffn`` and ``ops.moe_gated_ffn_backward``);
+``GatedFFN`` holds its two weights; ``GatedFFN.to_int8`` quantises their rows
+(``ops.moe_quant_int8``) for ``Int8GatedFFN``, which runs the routed int8 experts with one expert
+(``ops.moe_grouped_ffn_int8``).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import ops
+
+
+class _GatedFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w13, w2, activation):
+        if not any(ctx.needs_input_grad[:3]):
+            return ops.moe_gated_ffn(x, w13, w2, activation)
+        y, h = ops.moe_gated_ffn(x, w13, w2, activation, save_h=True)
+        ctx.save_for_backward(x, w13, w2, h)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w13, w2, h = ctx.saved_tensors
+        grads = ops.moe_gated_ffn_backward(dy.contiguous(), x, w13, w2, h, ctx.activation,
+                                           need=ctx.needs_input_grad[:3])
+        return (*grads, None)
+
+
+def gated_ffn(x, w13, w2, activation: str = "silu"):
+    """(act(x Wg^T) * (x Wu^T)) W2^T for x [..., d] in bf16 or fp16, with first-order gradients for
+    x, w13 [2F, d] and w2 [d, F]. The pre-activations are kept for the backward pass when one of
+    them asks for a gradient. (Capturing the backward pass into a CUDA graph follows torch's rule:
+    no eager graph of the same leaves may be alive during the capture.)"""
+    y = _GatedFFN.apply(x.reshape(-1, x.shape[-1]).contiguous(), w13, w2, activation)
+    return y.reshape(x.shape)
+
+
+class GatedFFN(torch.nn.Module):
+    """A gated FFN of hidden size d and width F; w13 = [gate; up] [2F, d], w2 [d, F]."""
+
+    def __init__(self, d: int, F: int, activation: str = "silu", dtype=torch.bfloat16,
+                 device="cuda"):
+        super().__init__()
+        if activation not in ops.ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ops.ACTIVATIONS)}")
+        self.activation = activation
+        self.w13 = torch.nn.Parameter(torch.empty(2 * F, d, dtype=dtype, device=device))
+        self.w2 = torch.nn.Parameter(torch.empty(d, F, dtype=dtype, device=device))
+        with torch.no_grad():
+            self.w13.normal_(0.0, 1 / math.sqrt(d))
+            self.w2.normal_(0.0, 1 / math.sqrt(F))
+
+    def forward(self, x):
+        return gated_ffn(x, self.w13, self.w2, self.activation)
+
+    def to_int8(self) -> "Int8GatedFFN":
+        """The serving form: one int8 scale per output channel. SiLU gates only (the routed
+        experts' activation)."""
+        if self.activation != "silu":
+            raise ValueError("the int8 experts are SwiGLU: activation must be 'silu'")
+        with torch.no_grad():
+            return Int8GatedFFN(*ops.moe_quant_int8(self.w13.detach()),
+                                *ops.moe_quant_int8(self.w2.detach()))
+
+
+class Int8GatedFFN:
+    """A W8A8 int8 SwiGLU FFN: codes w13 [2F, d], w2 [d, F] with scales [2F], [d]; bf16 tokens."""
+
+    def __init__(self, w13, w13_scale, w2, w2_scale):
+        self.weights = tuple(t.unsqueeze(0) for t in (w13, w13_scale, w2, w2_scale))
+        self.d, self.F = w2.shape
+
+    def __call__(self, x, dtype=torch.bfloat16):
+        """y [T, d] of x [T, d] bf16, summed in fp32 and rounded once to ``dtype``."""
+        T = x.shape[0]
+        offsets = torch.tensor([0, T], dtype=torch.int32).to(x.device, non_blocking=True)
+        perm = torch.arange(T, dtype=torch.int32, device=x.device)
+        out = ops.moe_grouped_ffn_int8(x, *self.weights, offsets, perm, 1)
+        return out[:T].to(dtype)

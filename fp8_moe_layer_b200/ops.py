@@ -542,3 +542,57 @@ class MoELayerFP8:
                            self.w13, self.w13_scale, self.w2, self.w2_scale, self.shape.k_max,
                            shared=self.shared, ws=self.ws, y=y, debug=debug,
                            stage_events=stage_events)
+
+
+class MoELayerInt8:
+    """Device-resident MoE layer with W8A8 int8 experts: ``MoELayerFP8`` with int8 codes in place of
+    e4m3, run through the split entry points (route, permute, grouped int8 FFN, combine).
+
+    router_w [E, d] and router_bias [E] (or None) fp32; w13 [E, 2F, d], w2 [E, d, F] int8 with scales
+    [E, 2F], [E, d]; shared = (w13 [2F, d], scale [2F], w2 [d, F], scale [d]) or None, an always-on
+    expert of weight 1. The layer owns one workspace: calls of one layer belong on one stream at a
+    time."""
+
+    def __init__(self, router_w, router_bias, k, k_max, w13, w13_scale, w2, w2_scale, shared=None):
+        if not 1 <= k <= k_max:
+            raise ValueError("k must lie in [1, k_max]")
+        self.router_w, self.router_bias = router_w, router_bias
+        self.k, self.k_max = int(k), int(k_max)
+        self.experts = (w13, w13_scale, w2, w2_scale)
+        self.E, self.d, self.F = w2.shape
+        self.shared = None if shared is None else tuple(t.unsqueeze(0) for t in shared)
+        self.ws, self._ident = None, {}
+
+    @classmethod
+    def from_weights(cls, router_w, router_bias, k, k_max, w13, w2, shared=None):
+        """The layer of bf16, fp16 or fp32 experts w13 [E, 2F, d], w2 [E, d, F] (and shared = (w13
+        [2F, d], w2 [d, F])), one int8 scale per output channel."""
+        if shared is not None:
+            shared = (*moe_quant_int8(shared[0]), *moe_quant_int8(shared[1]))
+        return cls(router_w, router_bias, k, k_max, *moe_quant_int8(w13), *moe_quant_int8(w2),
+                   shared=shared)
+
+    def _workspace(self, T, device):
+        dm = dims(T, self.d, self.E, self.F, self.k_max)
+        if self.ws is None or self.ws.numel() < workspace_bytes(dm):
+            self.ws = alloc_workspace(dm, device)
+        return self.ws
+
+    def __call__(self, hidden, k_per_token=None, k: Optional[int] = None):
+        """y bf16 [T, d]; per-token k from ``k_per_token`` if given, else the fixed ``k``."""
+        T, dev = hidden.shape[0], hidden.device
+        if T == 0:
+            return torch.empty_like(hidden)
+        k = self.k if k is None else int(k)
+        ws = self._workspace(T, dev)
+        ids, w = moe_route_topk(hidden, self.router_w, self.router_bias, k, k_per_token,
+                                self.k_max, F=self.F, ws=ws)
+        offsets, perm, inv = moe_permute(ids, k, k_per_token, self.E, d=self.d, F=self.F, ws=ws)
+        out = moe_grouped_ffn_int8(hidden, *self.experts, offsets, perm, self.k_max, ws=ws)
+        shared_out = None
+        if self.shared is not None:
+            if T not in self._ident:
+                self._ident[T] = (torch.tensor([0, T], dtype=torch.int32, device=dev),
+                                  torch.arange(T, dtype=torch.int32, device=dev))
+            shared_out = moe_grouped_ffn_int8(hidden, *self.shared, *self._ident[T], 1)
+        return moe_combine(out, w, inv, shared_out=shared_out)

@@ -94,7 +94,7 @@ def test_quant_int8_non_finite_rows(ops):
 
 
 # ------------------------------------------------------------------------------ int8 product
-MATMUL = [(1, 16, 16), (1, 4096, 1040), (2, 144, 272), (8, 48, 32), (9, 1040, 48), (16, 272, 144),
+MATMUL = [(1, 16, 16), (1, 4096, 1040), (2, 144, 272), (8, 48, 32), (9, 1040, 48), (16, 272, 144), (16, 4112, 272),
           (3, 528, 19504), (17, 2064, 528), (128, 512, 256), (77, 272, 19504), (100, 1040, 4912),
           (129, 528, 272), (300, 4112, 1040), (1003, 2064, 1040), (2100, 1024, 4144)]
 
@@ -177,7 +177,7 @@ def test_gated_ffn_backward(ops, T, d, F, dtype, act):
 # (T, d, E, F, k): decode tiles with a K split, ragged groups, experts without a token, prefill
 # tiles of 64 to 256 rows on one CTA and on pairs
 EXPERTS = [(1, 64, 8, 32, 2), (1, 2048, 128, 768, 8), (5, 528, 6, 272, 3), (64, 1024, 16, 528, 4),
-           (300, 528, 4, 336, 2), (700, 272, 3, 2064, 3), (2048, 256, 8, 208, 2),
+           (300, 528, 4, 336, 2), (700, 272, 3, 2064, 3), (1024, 272, 8, 2064, 2), (2048, 256, 8, 208, 2),
            (1500, 528, 7, 336, 3), (2100, 144, 16, 1040, 5)]
 
 
