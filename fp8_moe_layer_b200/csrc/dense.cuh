@@ -25,6 +25,11 @@ constexpr int kEpiRoutedDown = 5;   // row scale x column scale x D in fp32
 constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2;
 constexpr int kActSilu = 0, kActGeluTanh = 1;
 
+// How an operand lies: K-major, MN-major, or MN-major with its M or N a multiple of 64, which one box of
+// three dimensions fetches (64-element panels side by side) where the plain form takes two or more.
+constexpr int kMnNo = 0, kMnBoxes = 1, kMnPanels = 2;
+inline int dense_mn(int64_t rows) { return rows % 64 == 0 ? kMnPanels : kMnBoxes; }
+
 // One product of a launch. The maps' boxes are chosen by dense_maps for the launch's tile.
 struct DenseProblem {
   CUtensorMap a, b;
@@ -32,7 +37,7 @@ struct DenseProblem {
   CUtensorMap out_h;             // h or dh as [M][2][N] (the gated ones)
   CUtensorMap out16, out_h16;    // the same with 16-column boxes (split tiles, odd widths)
   int M, N, K;                   // valid sizes; gated: N = F (gate and up columns each)
-  int a_mn, b_mn;                // 1: the operand's contraction index is outermost
+  int a_mn, b_mn;                // kMn*: whether the operand's contraction index is outermost
   int m_tiles, n_tiles, num_kb, a_rows;  // set by launch_dense
   int tile0;                     // first tile of this product in the launch's tile list
 };
@@ -40,7 +45,7 @@ struct DenseProblem {
 constexpr int kMaxProblems = 3;
 struct DenseArgs {
   DenseProblem p[kMaxProblems];
-  int n_problems, total_tiles;
+  int n_problems, total_tiles;   // (total_tiles: set by the launch)
   int split, bn, direct;         // set by launch_dense
   int type, act;                 // 16-bit operands and outputs; int8: the output's type
   int save_h;                    // kEpiGated: write h
@@ -70,7 +75,7 @@ inline int64_t dense_a_rows(int64_t M) { return M >= 128 ? 128 : (M + 15) / 16 *
 
 // Tensor maps of one operand. rows x K elements of `bytes` (2 or 1) bytes, K-major unless mn.
 bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
-                       int type, bool mn, bool is_a, DenseTile tile);
+                       int type, int mn, bool is_a, DenseTile tile);
 // Gated weights [2][F][K].
 bool dense_map_gated_weights(CUtensorMap* m, const void* w13, int F, int K, int type, DenseTile tile);
 // The output maps that a problem's tile uses: out [M][N] and, for the gated epilogues, h or dh [M][2][N] (or null).

@@ -428,7 +428,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           uint8_t* sa = stages + stage * C::STAGE_BYTES;
           uint8_t* sb = sa + C::A_BYTES;
           if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (P.a_rows + nb_rows) * 128);
-          if (!C::I8 && a_mn) {
+          if (!C::I8 && a_mn == kMnPanels) {
+            load3(sa, &P.a, stage, 0, kb * 64, m0 / 64, pol);
+          } else if (!C::I8 && a_mn) {
             load2(sa, &P.a, stage, m0, kb * 64, pol);
             load2(sa + 8192, &P.a, stage, m0 + 64, kb * 64, pol);
           } else {
@@ -446,6 +448,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
               load3(sb, &P.b, stage, kb * C::KE, nt * (bn / 2), 0, pol);
               load3(sb + bn * 64, &P.b, stage, kb * C::KE, nt * (bn / 2), 1, pol);
             }
+          } else if (!C::I8 && b_mn == kMnPanels) {
+            load3(sb, &P.b, stage, 0, kb * 64, n0 / 64, pol);
           } else if (!C::I8 && b_mn) {
 #pragma unroll
             for (int i = 0; i < C::NB / 64; ++i)
@@ -483,11 +487,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       const uint32_t empty_p = PAIR ? cluster_addr(empty, 1) : 0u;
       const uint32_t tfull_l = PAIR ? cluster_addr(tfull, 0) : 0u;
       const uint32_t tfull_p = PAIR ? cluster_addr(tfull, 1) : 0u;
-      for (int tile = unit; ok && tile < total_tiles; tile += nunits, ++t) {
+      for (int tile = unit; ok && tile < total_tiles; tile += nunits) {
         int pi, mt, nt;
         tile_at(tile, pi, mt, nt);
         if constexpr (kRouted) pi = 0;
-        const int a_mn = C::I8 ? 0 : args.p[pi].a_mn, b_mn = C::I8 ? 0 : args.p[pi].b_mn;
+        const int a_mn = C::I8 ? 0 : args.p[pi].a_mn != 0, b_mn = C::I8 ? 0 : args.p[pi].b_mn != 0;
         const int kb0 = SPLIT ? args.p[pi].num_kb * srank / split : 0;
         const int kb1 = SPLIT ? args.p[pi].num_kb * (srank + 1) / split : args.p[pi].num_kb;
         const uint32_t idesc =
@@ -495,6 +499,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                   : idesc_f16_f32(args.type == kBf16, PAIR ? 256 : 128, bn, a_mn, b_mn);
         const int buf = t & 1;
         const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
+        ++t;
         const bool freed = PAIR ? mbar_wait_cluster(&tempty[buf], tph ^ 1u)
                                 : mbar_wait(&tempty[buf], tph ^ 1u);
         if (!freed) {
@@ -555,12 +560,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     uint8_t* mybuf = staging + (warp - 4) * C::WARP_STG;
     bool bad = false;
     int t = 0, nb = 0;          // tiles done; 16-column units stored so far
-    for (int tile = unit; tile < total_tiles && !bad; tile += nunits, ++t) {
+    for (int tile = unit; tile < total_tiles && !bad; tile += nunits) {
       int pi, mt, nt;
       tile_at(tile, pi, mt, nt);
       const DenseProblem& P = args.p[kRouted ? 0 : pi];
       const int buf = t & 1;
       const uint32_t tph = (static_cast<uint32_t>(t) >> 1) & 1u;
+      ++t;
       const int row0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + 32 * q +
                        (kRouted ? s_off[pi] : 0);
       const int row = row0 + lane;
@@ -931,8 +937,15 @@ DenseTile dense_tile(int epi, const int (*mnk)[3], int n) {
 }
 
 bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int type_bytes,
-                       int type, bool mn, bool is_a, DenseTile tile) {
-  if (mn) {         // [K][rows]: box 64 elements x 64 of K
+                       int type, int mn, bool is_a, DenseTile tile) {
+  const uint32_t staged = is_a ? 128u : (uint32_t)(tile.pair ? tile.bn / 2 : tile.bn);
+  if (mn == kMnPanels) {   // [K][rows] as panels [rows / 64][K][64]: all of a stage's in one box
+    const uint64_t dims[3] = {64, (uint64_t)K, (uint64_t)rows / 64};
+    const uint64_t str[2] = {(uint64_t)rows * type_bytes, 64ull * type_bytes};
+    const uint32_t box[3] = {64, 64, staged / 64};
+    return make_map(m, base, 3, dims, str, box, map_type(type));
+  }
+  if (mn) {                // [K][rows]: box 64 elements x 64 of K
     const uint64_t dims[2] = {(uint64_t)rows, (uint64_t)K};
     const uint64_t str[1] = {(uint64_t)rows * type_bytes};
     const uint32_t box[2] = {64, 64};
@@ -941,8 +954,7 @@ bool dense_map_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K
   const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
   const uint64_t str[1] = {(uint64_t)K * type_bytes};
   const uint32_t box[2] = {(uint32_t)(128 / type_bytes),
-                           is_a ? (uint32_t)dense_a_rows(rows)
-                                : (uint32_t)(tile.pair ? tile.bn / 2 : tile.bn)};
+                           is_a ? (uint32_t)dense_a_rows(rows) : staged};
   return make_map(m, base, 2, dims, str, box,
                   type_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(type));
 }

@@ -114,7 +114,7 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   g.M = T;
   g.N = F;
   g.K = d;
-  if (!dense_map_operand(&g.a, x, T, d, 2, type, false, true, tile) ||
+  if (!dense_map_operand(&g.a, x, T, d, 2, type, kMnNo, true, tile) ||
       !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
       !dense_map_outputs(&g, tile, act, T, F, type, true, h))
     return MOE_ERR_UNSUPPORTED;
@@ -129,8 +129,8 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   o.M = T;
   o.N = d;
   o.K = F;
-  if (!dense_map_operand(&o.a, act, T, F, 2, type, false, true, tile) ||
-      !dense_map_operand(&o.b, w2, d, F, 2, type, false, false, tile) ||
+  if (!dense_map_operand(&o.a, act, T, F, 2, type, kMnNo, true, tile) ||
+      !dense_map_operand(&o.b, w2, d, F, 2, type, kMnNo, false, tile) ||
       !dense_map_outputs(&o, tile, y, T, d, type, false, nullptr))
     return MOE_ERR_UNSUPPORTED;
   return launch_dense(kEpiStore, tile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -180,9 +180,9 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   g.M = T;
   g.N = F;
   g.K = d;
-  g.b_mn = 1;
-  if (!dense_map_operand(&g.a, dy, T, d, 2, type, false, true, tile) ||
-      !dense_map_operand(&g.b, w2, F, d, 2, type, true, false, tile) ||
+  g.b_mn = dense_mn(F);
+  if (!dense_map_operand(&g.a, dy, T, d, 2, type, kMnNo, true, tile) ||
+      !dense_map_operand(&g.b, w2, F, d, 2, type, g.b_mn, false, tile) ||
       !dense_map_outputs(&g, tile, act, T, F, type, true, dh))
     return MOE_ERR_UNSUPPORTED;
   if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
@@ -215,10 +215,10 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
     o.M = pr.M;
     o.N = pr.N;
     o.K = pr.K;
-    o.a_mn = pr.a_mn;
-    o.b_mn = 1;
-    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, pr.a_mn, true, wtile) ||
-        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, true, false, wtile) ||
+    o.a_mn = pr.a_mn ? dense_mn(pr.M) : kMnNo;
+    o.b_mn = dense_mn(pr.N);
+    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, o.a_mn, true, wtile) ||
+        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, o.b_mn, false, wtile) ||
         !dense_map_outputs(&o, wtile, pr.out, pr.M, pr.N, type, false, nullptr))
       return MOE_ERR_UNSUPPORTED;
   }

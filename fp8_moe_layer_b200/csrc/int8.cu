@@ -248,8 +248,8 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
   const DenseTile tile = dense_tile(kEpiInt8, mnk, 1);
   DenseArgs a{};
   DenseProblem& d = a.p[0];
-  if (!dense_map_operand(&d.a, codes, T, K, 1, 0, false, true, tile) ||
-      !dense_map_operand(&d.b, w, N, K, 1, 0, false, false, tile) ||
+  if (!dense_map_operand(&d.a, codes, T, K, 1, 0, kMnNo, true, tile) ||
+      !dense_map_operand(&d.b, w, N, K, 1, 0, kMnNo, false, tile) ||
       !dense_map_outputs(&d, tile, out, T, N, out_type, false, nullptr))
     return MOE_ERR_UNSUPPORTED;
   d.M = T;

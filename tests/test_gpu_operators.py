@@ -132,7 +132,7 @@ def test_matmul_int8_of_codes_extreme_values(ops, T, out_dtype):
 
 # ------------------------------------------------------------------------------ gated FFN
 FFN = [(1, 16, 16), (1, 1040, 784), (3, 64, 48), (9, 528, 112), (16, 144, 19504), (31, 272, 144), (128, 256, 256), (129, 144, 80),
-       (257, 528, 336), (500, 2048, 784), (1000, 1040, 2064)]
+       (257, 528, 336), (500, 2048, 784), (1000, 1040, 2064), (320, 1024, 576)]
 
 
 def ffn_inputs(T, d, F, dt, seed):
