@@ -68,8 +68,9 @@ struct DenseTile {
   int bn, split;
   bool direct;
 };
-// The tile for a launch of n products of sizes {M, N, K} (gated: N = F) with epilogue `epi`.
-DenseTile dense_tile(int epi, const int (*mnk)[3], int n);
+// The tile for a launch of n products of sizes {M, N, K} (gated: N = F) with epilogue `epi`, and its
+// estimated time in cycles.
+DenseTile dense_tile(int epi, const int (*mnk)[3], int n, double* cost = nullptr);
 // Rows of A fetched per box: 128, or all of them rounded up to 16.
 inline int64_t dense_a_rows(int64_t M) { return M >= 128 ? 128 : (M + 15) / 16 * 16; }
 
@@ -105,7 +106,9 @@ struct FewRowsArgs {
   int clear_status;              // this launch is the first of its call
   int x_stride;                  // set by launch_few_rows: pitch of x in shared memory, 0 = left in L2
 };
-// Whether kEpiInt8 can quantise T tokens of K elements itself.
+// Whether these kernels are the faster ones for T tokens and N rows (features) of K.
+bool few_rows_wins(int epi, int T, int N, int K);
+// Whether kEpiInt8 quantises T tokens of K elements itself.
 bool few_rows_quantises(int T, int K);
 cudaError_t launch_few_rows(int epi, const FewRowsArgs& args, cudaStream_t s);
 

@@ -284,10 +284,28 @@ __global__ void __launch_bounds__(256, 1) few_rows_kernel(const FewRowsArgs a) {
 
 // Pitch of a token in shared memory: 64 bytes modulo 128, so that eight tokens' pieces fall into
 // different banks.
-static int64_t few_pitch(int kbytes) { return ((int64_t)kbytes + 127) / 128 * 128 + 64; }
+static int64_t few_pitch(int64_t kbytes) { return (kbytes + 127) / 128 * 128 + 64; }
 
 bool few_rows_quantises(int T, int K) {
-  return T <= 8 && T * few_pitch(K) <= FewCfg<kEpiInt8, 1>::XBYTES;
+  // (every block quantises all tokens: with more than two a warp takes each, which 16384 elements hide)
+  return T <= 8 && (T <= 2 || T * (int64_t)K <= 16384) &&
+         T * few_pitch(K) <= FewCfg<kEpiInt8, 1>::XBYTES;
+}
+
+bool few_rows_wins(int epi, int T, int N, int K) {
+  if (T > kFewRows) return false;
+  // Microseconds, from whole calls at T = 1 to 64 on matrices of 3, 29, 117 and 352 MB: these kernels
+  // stream weights at 5.7 TB/s, less where 16 token columns or tokens read from L2 slow the consumers;
+  // the tcgen05 tiles at 5.0 TB/s with a 3 us longer start (T = 16, d = 4096, F = 14336 in bf16: 105 us
+  // here, 71 there; T = 1: 61 and 70; d = 2048, F = 768, T = 16: 9.5 and 13.9).
+  const int bytes_per = epi == kEpiInt8 ? 1 : 2;
+  const double mb = 1e-6 * N * (double)K * bytes_per * (epi == kEpiGated ? 2 : 1);
+  const bool two = T > 8;
+  const int64_t room = epi == kEpiGated ? (two ? FewCfg<kEpiGated, 2>::XBYTES : FewCfg<kEpiGated, 1>::XBYTES)
+                                        : (two ? FewCfg<kEpiStore, 2>::XBYTES : FewCfg<kEpiStore, 1>::XBYTES);
+  const bool staged = T * few_pitch((int64_t)K * bytes_per) <= room;
+  const double slow = staged ? (two ? 1.3 : 1.0) : (two ? 1.65 : 1.3);
+  return mb * slow / 5.7 <= mb / 5.0 + 3.0;
 }
 
 namespace {
@@ -305,7 +323,7 @@ cudaError_t launch_few(FewRowsArgs a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     attr_set[dev] = true;
   }
-  const int64_t pitch = few_pitch(a.K * (EPI == kEpiInt8 ? 1 : 2));
+  const int64_t pitch = few_pitch((int64_t)a.K * (EPI == kEpiInt8 ? 1 : 2));
   a.x_stride = a.T * pitch <= C::XBYTES ? (int)pitch : 0;
   const int smem = C::HEAD + C::PART + C::RING + a.x_stride * a.T;
   launch_pdl(few_rows_kernel<EPI, NT>, dim3(std::min(num_sms(), a.N)), dim3(32 * kFewWarps), smem, s, a);

@@ -3,7 +3,7 @@
 //
 //   forward   1. h = x W13^T, act = f(h_gate) h_up           (one kernel, kEpiGated)
 //             2. y = act W2^T                                 (kEpiStore)
-//             (T <= 16: the same two steps by the few-row kernels, few_rows.cu)
+//             (few tokens: either step by the few-token kernels, few_rows.cu)
 //   backward  1. dy W2, fused with h: dh and act              (one kernel, kEpiGatedGrad)
 //             2. dW13 = dh^T x, dW2 = dy^T act, dx = dh W13   (one launch, longest products first)
 #include <algorithm>
@@ -75,7 +75,8 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
   int* status = reinterpret_cast<int*>(base);
   uint16_t* act = reinterpret_cast<uint16_t*>(base + p.off_act);
 
-  if (T <= kFewRows) {
+  // each half by the few-token kernel or by the dense GEMM
+  if (few_rows_wins(kEpiGated, T, F, d)) {
     FewRowsArgs f{};
     f.x = x;
     f.w = w13;
@@ -89,38 +90,40 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
     f.status = status;
     f.clear_status = 1;
     if (launch_few_rows(kEpiGated, f, s) != cudaSuccess) return MOE_ERR_CUDA;
-    FewRowsArgs o{};
-    o.x = act;
-    o.w = w2;
-    o.T = T;
-    o.N = d;
-    o.K = F;
-    o.type = type;
-    o.out = y;
-    o.status = status;
-    return launch_few_rows(kEpiStore, o, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  } else {
+    const int mnk[1][3] = {{T, F, d}};
+    const DenseTile tile = dense_tile(kEpiGated, mnk, 1);
+    DenseArgs a{};
+    a.n_problems = 1;
+    a.type = type;
+    a.act = dims->act;
+    a.clear_status = 1;
+    a.save_h = h != nullptr;
+    a.status = status;
+    DenseProblem& g = a.p[0];
+    g.M = T;
+    g.N = F;
+    g.K = d;
+    if (!dense_map_operand(&g.a, x, T, d, 2, type, kMnNo, true, tile) ||
+        !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
+        !dense_map_outputs(&g, tile, act, T, F, type, true, h))
+      return MOE_ERR_UNSUPPORTED;
+    if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
-
-  const int mnk1[1][3] = {{T, F, d}}, mnk2[1][3] = {{T, d, F}};
-  DenseTile tile = dense_tile(kEpiGated, mnk1, 1);
-  DenseArgs a{};
-  a.n_problems = 1;
-  a.type = type;
-  a.act = dims->act;
-  a.clear_status = 1;
-  a.save_h = h != nullptr;
-  a.status = status;
-  DenseProblem& g = a.p[0];
-  g.M = T;
-  g.N = F;
-  g.K = d;
-  if (!dense_map_operand(&g.a, x, T, d, 2, type, kMnNo, true, tile) ||
-      !dense_map_gated_weights(&g.b, w13, F, d, type, tile) ||
-      !dense_map_outputs(&g, tile, act, T, F, type, true, h))
-    return MOE_ERR_UNSUPPORTED;
-  if (launch_dense(kEpiGated, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
-
-  tile = dense_tile(kEpiStore, mnk2, 1);
+  if (few_rows_wins(kEpiStore, T, d, F)) {
+    FewRowsArgs f{};
+    f.x = act;
+    f.w = w2;
+    f.T = T;
+    f.N = d;
+    f.K = F;
+    f.type = type;
+    f.out = y;
+    f.status = status;
+    return launch_few_rows(kEpiStore, f, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  const int mnk[1][3] = {{T, d, F}};
+  const DenseTile tile = dense_tile(kEpiStore, mnk, 1);
   DenseArgs b{};
   b.n_problems = 1;
   b.type = type;
@@ -188,41 +191,54 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   if (launch_dense(kEpiGatedGrad, tile, a, s) != cudaSuccess) return MOE_ERR_CUDA;
 
   // The products that follow are one launch, the longest K first: together they fill the last wave
-  // better than three.
+  // better than three. With few tokens dx is a few tiles of a very long K, which would run on long after
+  // the others; it then goes alone, its K split (T = 16, d = 4096, F = 14336: 315 -> 159 us). The choice
+  // goes by all three sizes, so a gradient does not depend on which others are wanted.
   struct Product {
     const void *a, *b;
     void* out;
     int M, N, K, a_mn;
   };
-  Product all[3] = {{dh, x, dw13, 2 * F, d, T, 1},
-                    {dy, act, dw2, d, F, T, 1},
-                    {dh, w13, dx, T, d, 2 * F, 0}};
-  if (2 * F > T) std::rotate(all, all + 2, all + 3);
-  // (the tile goes by all three sizes, so a gradient does not depend on which others are wanted)
+  const Product all[3] = {{dh, w13, dx, T, d, 2 * F, 0},
+                          {dh, x, dw13, 2 * F, d, T, 1},
+                          {dy, act, dw2, d, F, T, 1}};
   int sizes[3][3];
   for (int i = 0; i < 3; ++i) {
     sizes[i][0] = all[i].M;
     sizes[i][1] = all[i].N;
     sizes[i][2] = all[i].K;
   }
-  const DenseTile wtile = dense_tile(kEpiStore, sizes, 3);
-  DenseArgs b{};
-  b.type = type;
-  b.status = status;
-  for (const Product& pr : all) {
-    if (!pr.out) continue;
-    DenseProblem& o = b.p[b.n_problems++];
-    o.M = pr.M;
-    o.N = pr.N;
-    o.K = pr.K;
-    o.a_mn = pr.a_mn ? dense_mn(pr.M) : kMnNo;
-    o.b_mn = dense_mn(pr.N);
-    if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, o.a_mn, true, wtile) ||
-        !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, o.b_mn, false, wtile) ||
-        !dense_map_outputs(&o, wtile, pr.out, pr.M, pr.N, type, false, nullptr))
-      return MOE_ERR_UNSUPPORTED;
-  }
-  return launch_dense(kEpiStore, wtile, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  auto launch = [&](const int* which, int n, DenseTile t) {
+    DenseArgs b{};
+    b.type = type;
+    b.status = status;
+    for (int i = 0; i < n; ++i) {
+      const Product& pr = all[which[i]];
+      if (!pr.out) continue;
+      DenseProblem& o = b.p[b.n_problems++];
+      o.M = pr.M;
+      o.N = pr.N;
+      o.K = pr.K;
+      o.a_mn = pr.a_mn ? dense_mn(pr.M) : kMnNo;
+      o.b_mn = dense_mn(pr.N);
+      if (!dense_map_operand(&o.a, pr.a, pr.M, pr.K, 2, type, o.a_mn, true, t) ||
+          !dense_map_operand(&o.b, pr.b, pr.N, pr.K, 2, type, o.b_mn, false, t) ||
+          !dense_map_outputs(&o, t, pr.out, pr.M, pr.N, type, false, nullptr))
+        return MOE_ERR_UNSUPPORTED;
+    }
+    if (b.n_problems == 0) return MOE_OK;
+    return launch_dense(kEpiStore, t, b, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  };
+  double together = 0.0, alone = 0.0, rest = 0.0;
+  const DenseTile t3 = dense_tile(kEpiStore, sizes, 3, &together);
+  const DenseTile t1 = dense_tile(kEpiStore, sizes, 1, &alone);
+  const DenseTile t2 = dense_tile(kEpiStore, sizes + 1, 2, &rest);
+  constexpr double kLaunch = 5000.0;               // a further launch: its start and its first loads
+  static const int kWeightsFirst[3] = {1, 2, 0}, kTokensFirst[3] = {0, 1, 2};
+  if (together <= alone + rest + kLaunch)
+    return launch(2 * F > T ? kTokensFirst : kWeightsFirst, 3, t3);
+  rc = launch(kTokensFirst, 1, t1);
+  return rc != MOE_OK ? rc : launch(kWeightsFirst, 2, t2);
 }
 
 }  // extern "C"

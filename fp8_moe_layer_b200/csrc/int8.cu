@@ -221,7 +221,7 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
   int8_t* q = reinterpret_cast<int8_t*>(base + p.off_codes);
   float* sx = reinterpret_cast<float*>(base + p.off_scale);
   // a few tokens are quantised by the product's own blocks
-  const bool few = T <= kFewRows, fused = few && x && few_rows_quantises(T, K);
+  const bool few = few_rows_wins(kEpiInt8, T, N, K), fused = few && x && few_rows_quantises(T, K);
   if (x && !fused) {                               // (the quantisation clears the status word)
     if (launch_quant_int8(T, K, x_type, x, q, sx, status, s) != cudaSuccess) return MOE_ERR_CUDA;
     codes = q;
