@@ -9,6 +9,8 @@
 //                  dL/du = D f(g); dh = [dL/dg | dL/du] and a rounded once to the operands' type
 //   kEpiStore      D rounded once
 //   kEpiInt8       out = s_x[t] s_w[n] D[t, n] (+ bias[n]), D an exact int32 sum
+//   kEpiRouted*    the routed int8 experts: rows of A grouped by expert, each group with its own B;
+//                  act = silu(gate) up in fp32 with each row's maximum, and the scaled down product
 //
 // Orientation: the MMA's M (TMEM lanes) are the rows of A (tokens), its N the rows of B, so an
 // epilogue thread owns one token's consecutive columns: 16-byte pieces of 128-byte-swizzled rows of
@@ -24,10 +26,20 @@
 //           128 of B per K-block (32 KB) for 256 x 256 of product, so a byte of shared memory
 //           feeds twice the work of a 128 x 128 tile;
 //   single  128 x 64, 128 or 256 on one CTA: fewer rows than a pair would fill, or so few tiles that
-//           smaller ones occupy more SMs;
-//           (for at most 128 rows of A any multiple of 16 columns that deals the columns out evenly);
+//           smaller ones occupy more SMs (for at most 128 rows of A any multiple of 16 columns that
+//           deals the columns out evenly);
 //   split   a single tile whose K is shared by a cluster of 2, 4 or 8 CTAs, when even those leave SMs
 //           idle: the partial sums meet through distributed shared memory, no workspace, no counters.
+//
+// What bounds it, and what it measured:
+//   T = 8192, d = 7168, F = 2048 (bf16): power. Over seconds (SM clock 1.4 GHz under the 1000 W cap) the
+//   forward pass runs at 1.22 PFLOP/s and the backward pass at 1.14; cuBLAS's plain products of the same
+//   sizes at 1.25 to 1.34 and 1.23. The int8 product runs at 2.68 POP/s (K = 7168, N = 4096), torch._int_mm at
+//   2.88. Per 128-byte K-block the MMA thread issues in 534 cycles (512 at the peak rate) and waits
+//   another 12 to 17 % for data: a CTA's TMA delivers 32 KB in 500 to 590 cycles.
+//   T = 64, K = 4096, N = 28672 in int8 (117 MB): HBM and the launch; 24 us of which the first data
+//   take 3 (cold descriptors and pages) and the last epilogue 2.
+//   Small sizes: latency; about 3 us to the first data, 0.24 us per K-block, 2 us of epilogue.
 #include <algorithm>
 
 #include "common.cuh"
@@ -67,7 +79,7 @@ struct DenseCfg {
   static_assert(STAGES >= 3, "pipeline too shallow");
   static_assert(!PAIR || (BN == 256 && !SPLIT), "pair tiles");
   static_assert(!ROUTED || PAIR, "routed tiles run on pairs");
-  static_assert(EPI != kEpiGated || BN >= 128, "a gated tile stages 64 features at a time");
+  static_assert(EPI != kEpiGated || BN >= 128, "gated tiles are planned for 64 features or more of room");
   // a split tile's partial sums wait in the (by then idle) stages
   static_assert(!SPLIT || STAGES * STAGE_BYTES >= 128 * BN * 4, "exchange buffer");
 };
@@ -413,11 +425,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int a_mn = P.a_mn, b_mn = P.b_mn;
         const int kb0 = SPLIT ? P.num_kb * srank / split : 0;
         const int kb1 = SPLIT ? P.num_kb * (srank + 1) / split : P.num_kb;
-        // One m-tile: every unit reads its own weight rows once, and units that walked K in step would
-        // ask for the same few columns of a power-of-two pitch at a time; each starts elsewhere.
-        const int turn = !PAIR && args.direct ? (unit * 5) % (kb1 - kb0) : 0;
-        for (int it = kb0; it < kb1; ++it) {
-          const int kb = it + turn < kb1 ? it + turn : it + turn - (kb1 - kb0);
+        for (int kb = kb0; kb < kb1; ++kb) {
           const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
                                 : mbar_wait(&empty[stage], phase ^ 1u);
           if (!got) {

@@ -9,6 +9,7 @@
  * `stream`, negative moe_status values for what the host can check. Every entry point with a
  * workspace clears its status word first (moe_grouped_ffn_int8 excepted); moe_device_status(ws, ...) reads it after the call.
  * Calls whose workspaces differ are independent; two calls that may overlap need two workspaces.
+ * Outputs must not overlap inputs or each other.
  */
 #ifndef FP8_MOE_OPS_H
 #define FP8_MOE_OPS_H
