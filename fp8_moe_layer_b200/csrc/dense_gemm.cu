@@ -164,7 +164,7 @@ __device__ __forceinline__ void finish16(const DenseArgs& args, const DenseProbl
                                          const uint4 (&h)[4], float (&v)[16], const float (&u)[16],
                                          uint8_t* buf, int& n) {
   constexpr bool kTwoHalves = EPI == kEpiGated || EPI == kEpiGatedGrad;
-  uint8_t* slot = buf + (n++ & 1) * (kTwoHalves ? 3072 : 2048);
+  uint8_t* slot = buf + (n++ & 1) * (kTwoHalves ? 3 * 1024 : 2 * 1024);
   float w0[16], w1[16], w2[16];                      // output, and the two halves of h or dh
   if constexpr (EPI == kEpiStore) {
 #pragma unroll

@@ -82,7 +82,7 @@ class Int8GatedFFN:
     def __call__(self, x, dtype=torch.bfloat16):
         """y [T, d] of x [T, d] bf16, summed in fp32 and rounded once to ``dtype``."""
         T = x.shape[0]
-        offsets = torch.tensor([0, T], dtype=torch.int32).to(x.device, non_blocking=True)
+        offsets = torch.arange(2, dtype=torch.int32, device=x.device) * T     # one expert's rows
         perm = torch.arange(T, dtype=torch.int32, device=x.device)
         out = ops.moe_grouped_ffn_int8(x, *self.weights, offsets, perm, 1)
         return out[:T].to(dtype)

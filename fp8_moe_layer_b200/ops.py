@@ -561,7 +561,7 @@ class MoELayerInt8:
         self.experts = (w13, w13_scale, w2, w2_scale)
         self.E, self.d, self.F = w2.shape
         self.shared = None if shared is None else tuple(t.unsqueeze(0) for t in shared)
-        self.ws, self._ident = None, {}
+        self.ws = None
 
     @classmethod
     def from_weights(cls, router_w, router_bias, k, k_max, w13, w2, shared=None):
@@ -591,8 +591,7 @@ class MoELayerInt8:
         out = moe_grouped_ffn_int8(hidden, *self.experts, offsets, perm, self.k_max, ws=ws)
         shared_out = None
         if self.shared is not None:
-            if T not in self._ident:
-                self._ident[T] = (torch.tensor([0, T], dtype=torch.int32, device=dev),
-                                  torch.arange(T, dtype=torch.int32, device=dev))
-            shared_out = moe_grouped_ffn_int8(hidden, *self.shared, *self._ident[T], 1)
+            one = torch.arange(2, dtype=torch.int32, device=dev) * T         # one expert's rows
+            shared_out = moe_grouped_ffn_int8(
+                hidden, *self.shared, one, torch.arange(T, dtype=torch.int32, device=dev), 1)
         return moe_combine(out, w, inv, shared_out=shared_out)

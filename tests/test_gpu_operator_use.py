@@ -220,6 +220,47 @@ def test_captured_and_replayed(ops, T):
         assert all(torch.equal(a, b) for a, b in zip(got, run()))
 
 
+def test_layers_and_training_step_in_a_graph(ops):
+    """MoELayerInt8, the int8 block, and a forward and backward pass of the 16-bit block, captured with
+    no eager graph of their leaves alive."""
+    from fp8_moe_layer_b200.gated_ffn import GatedFFN
+    g = gen(9)
+    T, d, F, E = 24, 144, 80, 4
+    layer = ops.MoELayerInt8.from_weights(
+        rnd(g, E, d) * 0.05, None, 2, 2, rnd(g, E, 2 * F, d) / d ** 0.5, rnd(g, E, d, F) / F ** 0.5,
+        shared=(rnd(g, 2 * F, d) / d ** 0.5, rnd(g, d, F) / F ** 0.5))
+    ffn = GatedFFN(d, F)
+    served = ffn.to_int8()
+    x = rnd(g, T, d).to(torch.bfloat16)
+    dy = rnd(g, T, d).to(torch.bfloat16)
+
+    def run():
+        for p in ffn.parameters():
+            p.grad = None
+        y = ffn(x)
+        y.backward(dy)
+        return [y.detach(), *(p.grad for p in ffn.parameters()), layer(x), served(x)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = run()
+    for seed in (1, 2):
+        x.copy_(rnd(gen(seed), T, d))
+        dy.copy_(rnd(gen(seed + 10), T, d))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        grads = [p.grad for p in ffn.parameters()]
+        assert all(torch.equal(a, b) for a, b in zip(got, run()))
+        for p, was in zip(ffn.parameters(), grads):
+            p.grad = was                                     # the graph's own gradient buffers
+
+
 def test_one_workspace_for_calls_in_sequence(ops):
     """The same caller-owned workspace through different operators and sizes."""
     ws = torch.full((1 << 24,), 0x55, dtype=torch.uint8, device="cuda")
