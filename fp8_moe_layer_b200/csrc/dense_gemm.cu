@@ -41,6 +41,7 @@
 //   take 3 (cold descriptors and pages) and the last epilogue 2.
 //   Small sizes: latency; about 3 us to the first data, 0.24 us per K-block, 2 us of epilogue.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dense.cuh"
@@ -229,23 +230,47 @@ __device__ __forceinline__ void finish16(const DenseArgs& args, const DenseProbl
 
 // The epilogue of a split tile: CTA s of the cluster takes the s-th share of the tile's columns (in
 // steps of 16) and adds the CTAs' partial sums from their shared memory in rank order (the result does
-// not depend on timing).
+// not depend on timing). What its column groups read from memory is asked for while the products run
+// (load); finish follows the cluster barrier.
 template <int EPI, int BN>
-__device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, int split, int srank,
-                                               uint8_t* parked, uint8_t* buf) {
-  constexpr bool I8 = EPI == kEpiInt8;
-  constexpr int COLS = EPI == kEpiGated ? BN / 2 : BN;   // output columns of the tile
-  int pi, mt, nt;
-  dense_tile_at(args, tile, pi, mt, nt);
-  const DenseProblem& P = args.p[pi];
-  const int rl = (threadIdx.x - 128) & 127;          // row of the tile
-  const int hf = (threadIdx.x - 128) >> 7;           // the quarter's two warps take groups in turn
-  const int lane = threadIdx.x & 31, row0 = mt * 128 + rl - lane;
-  if (row0 >= P.M) return;                           // (whole warp)
-  const float rs = I8 && row0 + lane < P.M ? args.row_scale[row0 + lane] : 0.f;
-  int n = 0;
-  const uint32_t base = smem_addr(parked);
-  auto sum16 = [&](int c, float (&v)[16]) {
+struct SplitEpilogue {
+  static constexpr bool I8 = EPI == kEpiInt8;
+  static constexpr int COLS = EPI == kEpiGated ? BN / 2 : BN;        // output columns of the tile
+  static constexpr int kMine = COLS < 128 ? 1 : COLS / 64;           // groups (split >= 2, two warps)
+  int pi, mt, nt, rl, hf, lane, row0;
+  float rs, cl[kMine], bl[kMine];
+  uint4 h[kMine][4];
+
+  __device__ __forceinline__ int group(int k, int split, int srank) const {
+    return srank + (2 * k + hf) * split;             // the quarter's two warps take groups in turn
+  }
+
+  __device__ __forceinline__ void load(const DenseArgs& args, int tile, int split, int srank) {
+    dense_tile_at(args, tile, pi, mt, nt);
+    const DenseProblem& P = args.p[pi];
+    rl = (threadIdx.x - 128) & 127;                  // row of the tile
+    hf = (threadIdx.x - 128) >> 7;
+    lane = threadIdx.x & 31;
+    row0 = mt * 128 + rl - lane;
+    rs = I8 && row0 + lane < P.M ? args.row_scale[row0 + lane] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int g = group(k, split, srank), col = nt * COLS + 16 * g;
+      const bool in = g < COLS / 16 && col < P.N;
+      cl[k] = bl[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[k][i] = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (I8) {
+        if (in) cl[k] = args.col_scale[col + (lane & 15)];
+        if (in && args.bias) bl[k] = args.bias[col + (lane & 15)];
+      } else if constexpr (EPI == kEpiGatedGrad) {
+        if (in && row0 + lane < P.M) load_h16(args.h, P.N, row0 + lane, col, h[k]);
+      }
+    }
+  }
+
+  // Sum over the CTAs of sixteen columns from c on.
+  __device__ __forceinline__ void sum16(uint32_t base, int split, int c, float (&v)[16]) const {
     int acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -270,36 +295,26 @@ __device__ __forceinline__ void split_epilogue(const DenseArgs& args, int tile, 
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __int2float_rn(acc[i]);
     }
-  };
-  // what the groups read from memory first, in one round of latency (split >= 2, and two warps)
-  constexpr int kMine = COLS < 128 ? 1 : COLS / 64;
-  float cl[kMine], bl[kMine];
-  uint4 h[kMine][4];
+  }
+
+  __device__ __forceinline__ void finish(const DenseArgs& args, int split, int srank, uint8_t* parked,
+                                         uint8_t* buf) const {
+    const DenseProblem& P = args.p[pi];
+    if (row0 >= P.M) return;                         // (whole warp)
+    const uint32_t base = smem_addr(parked);
+    int n = 0;
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int g = srank + (2 * k + hf) * split, col = nt * COLS + 16 * g;
-    const bool in = g < COLS / 16 && col < P.N;
-    cl[k] = bl[k] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[k][i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (I8) {
-      if (in) cl[k] = args.col_scale[col + (lane & 15)];
-      if (in && args.bias) bl[k] = args.bias[col + (lane & 15)];
-    } else if constexpr (EPI == kEpiGatedGrad) {
-      if (in && row0 + lane < P.M) load_h16(args.h, P.N, row0 + lane, col, h[k]);
+    for (int k = 0; k < kMine; ++k) {
+      const int c = 16 * group(k, split, srank), col = nt * COLS + c;
+      if (c >= COLS || col >= P.N) break;
+      float v[16], u[16];
+      sum16(base, split, c, v);
+      if constexpr (EPI == kEpiGated) sum16(base, split, COLS + c, u);
+      finish16<EPI>(args, P, row0, lane, col, rs, cl[k], bl[k], h[k], v, u, buf, n);
     }
+    if (lane == 0) bulk_wait_read_all();             // (the grid's end completes the stores)
   }
-#pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int c = 16 * (srank + (2 * k + hf) * split), col = nt * COLS + c;
-    if (c >= COLS || col >= P.N) break;
-    float v[16], u[16];
-    sum16(c, v);
-    if constexpr (EPI == kEpiGated) sum16(COLS + c, u);
-    finish16<EPI>(args, P, row0, lane, col, rs, cl[k], bl[k], h[k], v, u, buf, n);
-  }
-  if (lane == 0) bulk_wait_all();
-}
+};
 
 template <int EPI, bool PAIR, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kDenseThreads, 1)
@@ -408,7 +423,24 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if constexpr (PAIR) tma_load_3d_pair(dst, m, full_l + 8u * stage, x, y, z, pol);
     else tma_load_3d(dst, m, &full[stage], x, y, z, pol);
   };
+  // The operands' forms as one number, so that the producer's loop over K has them as constants: its
+  // thread issues 32 KB every 500 cycles, and reading the flags there cost 8 to 10 % of a 16-bit launch.
+  auto by_form = [&](const DenseProblem& P, auto&& body) {
+    if constexpr (C::I8 || kGatedCols) {
+      body(std::integral_constant<int, kMnNo>{}, std::integral_constant<int, kMnNo>{});
+    } else {
+      auto with_b = [&](auto am) {
+        if (P.b_mn == kMnNo) body(am, std::integral_constant<int, kMnNo>{});
+        else if (P.b_mn == kMnBoxes) body(am, std::integral_constant<int, kMnBoxes>{});
+        else body(am, std::integral_constant<int, kMnPanels>{});
+      };
+      if (P.a_mn == kMnNo) with_b(std::integral_constant<int, kMnNo>{});
+      else if (P.a_mn == kMnBoxes) with_b(std::integral_constant<int, kMnBoxes>{});
+      else with_b(std::integral_constant<int, kMnPanels>{});
+    }
+  };
 
+  [[maybe_unused]] SplitEpilogue<EPI, BN> split_epilogue;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -422,55 +454,59 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const DenseProblem& P = args.p[kRouted ? 0 : pi];
         const int m0 = (PAIR ? 2 * mt + static_cast<int>(crank) : mt) * 128 + (kRouted ? s_off[pi] : 0);
         const int n0 = nt * bn + static_cast<int>(crank) * C::NB;
-        const int a_mn = P.a_mn, b_mn = P.b_mn;
         const int kb0 = SPLIT ? P.num_kb * srank / split : 0;
         const int kb1 = SPLIT ? P.num_kb * (srank + 1) / split : P.num_kb;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
-                                : mbar_wait(&empty[stage], phase ^ 1u);
-          if (!got) {
-            report(args.status, kStatusDeviceTimeout, kWhereDense, 1);
-            ok = false;
-            break;
-          }
-          uint8_t* sa = stages + stage * C::STAGE_BYTES;
-          uint8_t* sb = sa + C::A_BYTES;
-          if (leader) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * (P.a_rows + nb_rows) * 128);
-          if (!C::I8 && a_mn == kMnPanels) {
-            load3(sa, &P.a, stage, 0, kb * 64, m0 / 64, pol);
-          } else if (!C::I8 && a_mn) {
-            load2(sa, &P.a, stage, m0, kb * 64, pol);
-            load2(sa + 8192, &P.a, stage, m0 + 64, kb * 64, pol);
-          } else {
-            load2(sa, &P.a, stage, kb * C::KE, m0, pol);
-          }
-          if constexpr (EPI == kEpiRoutedGated) {
-            tma_load_4d_pair(sb, &P.b, full_l + 8u * stage, kb * C::KE, nt * (BN / 2),
-                             static_cast<int>(crank), pi, pol);
-          } else if constexpr (EPI == kEpiRoutedDown) {
-            load3(sb, &P.b, stage, kb * C::KE, n0, pi, pol);
-          } else if constexpr (kGatedCols) {
-            if constexpr (PAIR) {
-              load3(sb, &P.b, stage, kb * C::KE, nt * (BN / 2), static_cast<int>(crank), pol);
-            } else {
-              load3(sb, &P.b, stage, kb * C::KE, nt * (bn / 2), 0, pol);
-              load3(sb + bn * 64, &P.b, stage, kb * C::KE, nt * (bn / 2), 1, pol);
+        const uint32_t tx = (PAIR ? 2 : 1) * (P.a_rows + nb_rows) * 128;
+        const CUtensorMap *ma = &P.a, *mb = &P.b;
+        by_form(P, [&](auto am, auto bm) {
+          constexpr int AM = decltype(am)::value, BM = decltype(bm)::value;
+          for (int kb = kb0; kb < kb1; ++kb) {
+            const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
+                                  : mbar_wait(&empty[stage], phase ^ 1u);
+            if (!got) {
+              report(args.status, kStatusDeviceTimeout, kWhereDense, 1);
+              ok = false;
+              break;
             }
-          } else if (!C::I8 && b_mn == kMnPanels) {
-            load3(sb, &P.b, stage, 0, kb * 64, n0 / 64, pol);
-          } else if (!C::I8 && b_mn) {
+            uint8_t* sa = stages + stage * C::STAGE_BYTES;
+            uint8_t* sb = sa + C::A_BYTES;
+            if (leader) mbar_arrive_expect_tx(&full[stage], tx);
+            if constexpr (AM == kMnPanels) {
+              load3(sa, ma, stage, 0, kb * 64, m0 / 64, pol);
+            } else if constexpr (AM == kMnBoxes) {
+              load2(sa, ma, stage, m0, kb * 64, pol);
+              load2(sa + 8192, ma, stage, m0 + 64, kb * 64, pol);
+            } else {
+              load2(sa, ma, stage, kb * C::KE, m0, pol);
+            }
+            if constexpr (EPI == kEpiRoutedGated) {
+              tma_load_4d_pair(sb, mb, full_l + 8u * stage, kb * C::KE, nt * (BN / 2),
+                               static_cast<int>(crank), pi, pol);
+            } else if constexpr (EPI == kEpiRoutedDown) {
+              load3(sb, mb, stage, kb * C::KE, n0, pi, pol);
+            } else if constexpr (kGatedCols) {
+              if constexpr (PAIR) {
+                load3(sb, mb, stage, kb * C::KE, nt * (BN / 2), static_cast<int>(crank), pol);
+              } else {
+                load3(sb, mb, stage, kb * C::KE, nt * (bn / 2), 0, pol);
+                load3(sb + bn * 64, mb, stage, kb * C::KE, nt * (bn / 2), 1, pol);
+              }
+            } else if constexpr (BM == kMnPanels) {
+              load3(sb, mb, stage, 0, kb * 64, n0 / 64, pol);
+            } else if constexpr (BM == kMnBoxes) {
 #pragma unroll
-            for (int i = 0; i < C::NB / 64; ++i)
-              load2(sb + i * 8192, &P.b, stage, n0 + 64 * i, kb * 64, pol);
-          } else {
-            load2(sb, &P.b, stage, kb * C::KE, n0, pol);
+              for (int i = 0; i < C::NB / 64; ++i)
+                load2(sb + i * 8192, mb, stage, n0 + 64 * i, kb * 64, pol);
+            } else {
+              load2(sb, mb, stage, kb * C::KE, n0, pol);
+            }
+            ++issued;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+        });
       }
       // the most recent load of every stage must land before the CTA exits (the odd CTA of a
       // pair relies on the final cluster barrier, which the even one reaches after this drain)
@@ -587,7 +623,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       // a 33 us launch at T = 64, N = 28672.
       constexpr int kChunks = C::I8 ? BN / 32 : 1;
       float cs[kChunks], cb[kChunks];
-      if constexpr (EPI == kEpiInt8) {
+      if constexpr (EPI == kEpiInt8 && !SPLIT) {
         rs = row < P.M ? args.row_scale[row] : 0.f;
 #pragma unroll
         for (int u = 0; u < kChunks; ++u) {
@@ -608,6 +644,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           cs[u] = col < P.N ? args.col_scale[(size_t)pi * ld + up + col] : 0.f;
         }
       }
+      if constexpr (SPLIT) split_epilogue.load(args, unit, split, srank);
       auto pick = [&](const float (&v)[kChunks], int u) {
         float x = v[0];
 #pragma unroll
@@ -870,14 +907,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         else mbar_arrive(&tempty[buf]);
       }
     }
-    if (kRouted || lane == 0) bulk_wait_all();       // this warp's stores have completed
+    // this warp's stores have read their buffers (the grid's end completes them)
+    if (kRouted || lane == 0) bulk_wait_read_all();
   }
 
   if constexpr (SPLIT) {
     // Every thread of the cluster passes both barriers, also after a timeout.
     cluster_sync_all();                              // all partial sums are parked
-    if (warp >= 4)
-      split_epilogue<EPI, BN>(args, unit, split, srank, stages, staging + (warp - 4) * C::WARP_STG);
+    if (warp >= 4) split_epilogue.finish(args, split, srank, stages, staging + (warp - 4) * C::WARP_STG);
   }
   tc_fence_before_sync();
   if constexpr (PAIR || SPLIT) cluster_sync_all();   // (no CTA leaves while another reads its sums)
