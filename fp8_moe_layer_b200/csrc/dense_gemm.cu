@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const uint32_t tx = (PAIR ? 2 : 1) * (P.a_rows + nb_rows) * 128;
         const CUtensorMap *ma = &P.a, *mb = &P.b;
         by_form(P, [&](auto am, auto bm) {
-          constexpr int AM = decltype(am)::value, BM = decltype(bm)::value;
+          [[maybe_unused]] constexpr int AM = decltype(am)::value, BM = decltype(bm)::value;
           for (int kb = kb0; kb < kb1; ++kb) {
             const bool got = PAIR ? mbar_wait_cluster(&empty[stage], phase ^ 1u)
                                   : mbar_wait(&empty[stage], phase ^ 1u);
