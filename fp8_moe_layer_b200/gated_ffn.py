@@ -19,8 +19,6 @@ from . import ops
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2, activation):
-        if not any(ctx.needs_input_grad[:3]):
-            return ops.moe_gated_ffn(x, w13, w2, activation)
         y, h = ops.moe_gated_ffn(x, w13, w2, activation, save_h=True)
         ctx.save_for_backward(x, w13, w2, h)
         ctx.activation = activation
@@ -40,7 +38,12 @@ def gated_ffn(x, w13, w2, activation: str = "silu"):
     x, w13 [2F, d] and w2 [d, F]. The pre-activations are kept for the backward pass when one of
     them asks for a gradient. (Capturing the backward pass into a CUDA graph follows torch's rule:
     no eager graph of the same leaves may be alive during the capture.)"""
-    y = _GatedFFN.apply(x.reshape(-1, x.shape[-1]).contiguous(), w13, w2, activation)
+    rows = x.reshape(-1, x.shape[-1]).contiguous()
+    # (asked here: inside the function torch reports the leaves' wishes under no_grad as well)
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, w13, w2)):
+        y = _GatedFFN.apply(rows, w13, w2, activation)
+    else:
+        y = ops.moe_gated_ffn(rows, w13, w2, activation)
     return y.reshape(x.shape)
 
 

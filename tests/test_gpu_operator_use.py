@@ -151,6 +151,23 @@ def test_gradients_against_differences(ops, act):
         assert abs(have - diff) <= room + 1e-5 * (1 + abs(diff)), (i, have, diff, room)
 
 
+def test_no_pre_activations_without_gradients(ops, monkeypatch):
+    """The block keeps h only where a backward pass can follow."""
+    from fp8_moe_layer_b200.gated_ffn import GatedFFN, gated_ffn
+    kept = []
+    real = ops.moe_gated_ffn
+    monkeypatch.setattr(ops, "moe_gated_ffn",
+                        lambda *a, save_h=False, **k: kept.append(save_h) or real(*a, save_h=save_h, **k))
+    ffn, x = GatedFFN(64, 48), torch.randn(5, 64, device="cuda").to(torch.bfloat16)
+    y = ffn(x)
+    with torch.no_grad():
+        assert torch.equal(ffn(x), y) and not ffn(x).requires_grad
+    with torch.inference_mode():
+        ffn(x)
+    gated_ffn(x, ffn.w13.detach(), ffn.w2.detach())
+    assert y.requires_grad and kept == [True, False, False, False, False]
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 def calls(ops, seed, T=40):
     """Every operator on inputs of one seed: (callable, inputs that a graph may refill)."""
