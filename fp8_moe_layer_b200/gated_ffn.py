@@ -28,7 +28,10 @@ class _GatedFFN(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, w13, w2, h = ctx.saved_tensors
-        grads = ops.moe_gated_ffn_backward(dy.contiguous(), x, w13, w2, h, ctx.activation,
+        dy = dy.contiguous()
+        if dy.data_ptr() % 16:                     # a slice of a larger gradient
+            dy = dy.clone()
+        grads = ops.moe_gated_ffn_backward(dy, x, w13, w2, h, ctx.activation,
                                            need=ctx.needs_input_grad[:3])
         return (*grads, None)
 

@@ -151,6 +151,18 @@ def test_gradients_against_differences(ops, act):
         assert abs(have - diff) <= room + 1e-5 * (1 + abs(diff)), (i, have, diff, room)
 
 
+def test_gradient_at_an_odd_offset(ops):
+    """A gradient that arrives as a slice behind one other element is not 16-byte aligned."""
+    from fp8_moe_layer_b200.gated_ffn import gated_ffn
+    x, w13, w2, dy = ffn_inputs(9, 64, 48, torch.bfloat16, 2)
+    a = x.clone().requires_grad_()
+    one = torch.ones(1, device="cuda", dtype=torch.bfloat16)
+    both = torch.cat([one, gated_ffn(a, w13, w2).reshape(-1)])
+    both.backward(torch.cat([one, dy.reshape(-1)]))
+    _, h = ops.moe_gated_ffn(x, w13, w2, save_h=True)
+    assert torch.equal(a.grad, ops.moe_gated_ffn_backward(dy, x, w13, w2, h)[0])
+
+
 def test_no_pre_activations_without_gradients(ops, monkeypatch):
     """The block keeps h only where a backward pass can follow."""
     from fp8_moe_layer_b200.gated_ffn import GatedFFN, gated_ffn
