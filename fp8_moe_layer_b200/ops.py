@@ -550,8 +550,8 @@ class MoELayerInt8:
 
     router_w [E, d] and router_bias [E] (or None) fp32; w13 [E, 2F, d], w2 [E, d, F] int8 with scales
     [E, 2F], [E, d]; shared = (w13 [2F, d], scale [2F], w2 [d, F], scale [d]) or None, an always-on
-    expert of weight 1. The layer owns one workspace: calls of one layer belong on one stream at a
-    time."""
+    expert of weight 1. Each call takes its own workspace from torch's allocator, so calls of one layer
+    may be captured or run on several streams; ``ws`` is the last call's (for ``device_status``)."""
 
     def __init__(self, router_w, router_bias, k, k_max, w13, w13_scale, w2, w2_scale, shared=None):
         if not 1 <= k <= k_max:
@@ -572,19 +572,13 @@ class MoELayerInt8:
         return cls(router_w, router_bias, k, k_max, *moe_quant_int8(w13), *moe_quant_int8(w2),
                    shared=shared)
 
-    def _workspace(self, T, device):
-        dm = dims(T, self.d, self.E, self.F, self.k_max)
-        if self.ws is None or self.ws.numel() < workspace_bytes(dm):
-            self.ws = alloc_workspace(dm, device)
-        return self.ws
-
     def __call__(self, hidden, k_per_token=None, k: Optional[int] = None):
         """y bf16 [T, d]; per-token k from ``k_per_token`` if given, else the fixed ``k``."""
         T, dev = hidden.shape[0], hidden.device
         if T == 0:
             return torch.empty_like(hidden)
         k = self.k if k is None else int(k)
-        ws = self._workspace(T, dev)
+        self.ws = ws = alloc_workspace(dims(T, self.d, self.E, self.F, self.k_max), dev)
         ids, w = moe_route_topk(hidden, self.router_w, self.router_bias, k, k_per_token,
                                 self.k_max, F=self.F, ws=ws)
         offsets, perm, inv = moe_permute(ids, k, k_per_token, self.E, d=self.d, F=self.F, ws=ws)

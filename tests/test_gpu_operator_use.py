@@ -290,6 +290,32 @@ def test_layers_and_training_step_in_a_graph(ops):
             p.grad = was                                     # the graph's own gradient buffers
 
 
+def test_captured_layer_outlives_larger_calls(ops):
+    """A captured call of MoELayerInt8 replays in memory of its own after a larger call and after other
+    tensors took what that one gave back."""
+    g = gen(3)
+    d, F, E = 144, 80, 4
+    layer = ops.MoELayerInt8.from_weights(rnd(g, E, d) * 0.05, None, 2, 2, rnd(g, E, 2 * F, d) / 12,
+                                          rnd(g, E, d, F) / 9)
+    x, big = rnd(g, 24, d).to(torch.bfloat16), rnd(g, 900, d).to(torch.bfloat16)
+    want = layer(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer(x)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        y = layer(x)
+    need = ops.workspace_bytes(ops.dims(24, d, E, F, 2))
+    layer(big)
+    other = [torch.full((need,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(bool((o == 0x5A).all()) for o in other)
+
+
 def test_one_workspace_for_calls_in_sequence(ops):
     """The same caller-owned workspace through different operators and sizes."""
     ws = torch.full((1 << 24,), 0x55, dtype=torch.uint8, device="cuda")
