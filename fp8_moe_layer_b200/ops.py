@@ -379,14 +379,18 @@ def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     if (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()
             and not p & 15):
         return p
+    _expect(name, t, dtype, shape, device)
+    raise ValueError(f"{name} must be contiguous" if not t.is_contiguous()
+                     else f"{name} must be 16-byte aligned")
+
+
+def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
-    raise ValueError(f"{name} must be contiguous" if not t.is_contiguous()
-                     else f"{name} must be 16-byte aligned")
 
 
 def _workspace(ws: Optional[torch.Tensor], need: int, where: str, device) -> torch.Tensor:
@@ -556,10 +560,17 @@ class MoELayerInt8:
     def __init__(self, router_w, router_bias, k, k_max, w13, w13_scale, w2, w2_scale, shared=None):
         if not 1 <= k <= k_max:
             raise ValueError("k must lie in [1, k_max]")
+        if w2.dim() != 3:
+            raise ValueError("w2 must be [E, d, F]")
+        E, d, F = w2.shape
+        _expect("router_w", router_w, torch.float32, (E, d), w2.device)
+        if router_bias is not None:
+            _expect("router_bias", router_bias, torch.float32, (E,), w2.device)
+        _expect("w13", w13, torch.int8, (E, 2 * F, d), w2.device)
         self.router_w, self.router_bias = router_w, router_bias
         self.k, self.k_max = int(k), int(k_max)
         self.experts = (w13, w13_scale, w2, w2_scale)
-        self.E, self.d, self.F = w2.shape
+        self.E, self.d, self.F = E, d, F
         self.shared = None if shared is None else tuple(t.unsqueeze(0) for t in shared)
         self.ws = None
 
@@ -574,10 +585,20 @@ class MoELayerInt8:
 
     def __call__(self, hidden, k_per_token=None, k: Optional[int] = None):
         """y bf16 [T, d]; per-token k from ``k_per_token`` if given, else the fixed ``k``."""
-        T, dev = hidden.shape[0], hidden.device
+        if hidden.dim() != 2:
+            raise ValueError("hidden must be [T, d]")
+        T, dev = hidden.shape[0], self.router_w.device
+        _expect("hidden", hidden, torch.bfloat16, (T, self.d), dev)
+        if k_per_token is not None:
+            _expect("k_per_token", k_per_token, torch.int32, (T,), dev)
+        k = self.k if k is None else int(k)
+        if not 1 <= k <= self.k_max:
+            raise ValueError("k must lie in [1, k_max]")
         if T == 0:
             return torch.empty_like(hidden)
-        k = self.k if k is None else int(k)
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self(hidden, k_per_token, k)
         self.ws = ws = alloc_workspace(dims(T, self.d, self.E, self.F, self.k_max), dev)
         ids, w = moe_route_topk(hidden, self.router_w, self.router_bias, k, k_per_token,
                                 self.k_max, F=self.F, ws=ws)

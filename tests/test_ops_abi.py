@@ -168,3 +168,27 @@ def test_binding_refuses_cpu_tensors(ops):
         ops.moe_gated_ffn(x.float(), f.float(), f.float())
     with pytest.raises(ValueError):
         ops.moe_gated_ffn(x, f, f, activation="relu")
+
+
+def test_int8_layer_refusals(ops):
+    """What would let the router read behind its weights, or a call misread its tokens."""
+    E, d, F = 3, 64, 32
+    rw, rb = torch.zeros(E, d), torch.zeros(E)
+    q = (torch.zeros(E, 2 * F, d, dtype=torch.int8), torch.ones(E, 2 * F),
+         torch.zeros(E, d, F, dtype=torch.int8), torch.ones(E, d))
+    layer = ops.MoELayerInt8(rw, rb, 2, 2, *q)
+    for exc, args in [(ValueError, (rw[:, :48], rb, 2, 2, *q)), (ValueError, (rw[:2], rb, 2, 2, *q)),
+                      (TypeError, (rw.double(), rb, 2, 2, *q)), (ValueError, (rw, rb[:2], 2, 2, *q)),
+                      (ValueError, (rw, None, 3, 2, *q)), (ValueError, (rw, None, 0, 2, *q)),
+                      (ValueError, (rw, rb, 2, 2, q[0][:, :F], *q[1:])),
+                      (ValueError, (rw, rb, 2, 2, *q[:2], q[2][0], q[3]))]:
+        with pytest.raises(exc):
+            ops.MoELayerInt8(*args)
+    x, kpt = torch.zeros(5, d, dtype=torch.bfloat16), torch.ones(5, dtype=torch.int32)
+    for exc, args, kw in [(TypeError, (x.half(),), {}), (ValueError, (x[:, :48],), {}),
+                          (ValueError, (x[0],), {}), (TypeError, (x, kpt.long()), {}),
+                          (ValueError, (x, kpt[:4]), {}), (ValueError, (x,), {"k": 3}),
+                          (ValueError, (x,), {"k": 0}),
+                          (ValueError, (x,), {})]:           # the last: not on a CUDA device
+        with pytest.raises(exc):
+            layer(*args, **kw)
