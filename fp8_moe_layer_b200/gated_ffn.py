@@ -86,9 +86,10 @@ class Int8GatedFFN:
         self.d, self.F = w2.shape
 
     def __call__(self, x, dtype=torch.bfloat16):
-        """y [T, d] of x [T, d] bf16, summed in fp32 and rounded once to ``dtype``."""
-        T = x.shape[0]
+        """y [..., d] of x [..., d] bf16, summed in fp32 and rounded once to ``dtype``."""
+        rows = x.reshape(-1, x.shape[-1]).contiguous()
+        T = rows.shape[0]
         offsets = torch.arange(2, dtype=torch.int32, device=x.device) * T     # one expert's rows
         perm = torch.arange(T, dtype=torch.int32, device=x.device)
-        out = ops.moe_grouped_ffn_int8(x, *self.weights, offsets, perm, 1)
-        return out[:T].to(dtype)
+        out = ops.moe_grouped_ffn_int8(rows, *self.weights, offsets, perm, 1)
+        return out[:T].to(dtype).reshape(x.shape)

@@ -163,6 +163,17 @@ def test_gradient_at_an_odd_offset(ops):
     assert torch.equal(a.grad, ops.moe_gated_ffn_backward(dy, x, w13, w2, h)[0])
 
 
+def test_int8_block_takes_the_shapes_of_the_16_bit_block(ops):
+    from fp8_moe_layer_b200.gated_ffn import GatedFFN
+    ffn = GatedFFN(64, 48)
+    q, x = ffn.to_int8(), torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    flat = q(x.view(12, 64))
+    for v in (x, x.transpose(0, 1), x[:, :0], x[0, 0]):
+        assert q(v).shape == ffn(v).shape == v.shape
+    assert torch.equal(q(x).view(12, 64), flat)
+    assert torch.equal(q(x.transpose(0, 1)).transpose(0, 1).reshape(12, 64), flat)
+
+
 def test_no_pre_activations_without_gradients(ops, monkeypatch):
     """The block keeps h only where a backward pass can follow."""
     from fp8_moe_layer_b200.gated_ffn import GatedFFN, gated_ffn
