@@ -33,10 +33,10 @@
 //
 // What bounds it, and what it measured:
 //   T = 8192, d = 7168, F = 2048 (bf16): power. Over seconds (SM clock 1.4 GHz under the 1000 W cap) the
-//   forward pass runs at 1.22 PFLOP/s and the backward pass at 1.14; cuBLAS's plain products of the same
-//   sizes at 1.25 to 1.34 and 1.23. The int8 product runs at 2.68 POP/s (K = 7168, N = 4096), torch._int_mm at
-//   2.88. Per 128-byte K-block the MMA thread issues in 534 cycles (512 at the peak rate) and waits
-//   another 12 to 17 % for data: a CTA's TMA delivers 32 KB in 500 to 590 cycles.
+//   forward pass runs at 1.18 PFLOP/s and the backward pass at 1.15; cuBLAS's plain products of the same
+//   sizes at 1.19 to 1.30. The int8 product runs at 2.62 POP/s (K = 7168, N = 4096), torch._int_mm at
+//   2.78. Per 128-byte K-block the MMA thread issues in 534 cycles (512 at the peak rate) and waits
+//   another 12 % for data: a CTA's TMA delivers 32 KB in about 500 cycles.
 //   T = 64, K = 4096, N = 28672 in int8 (117 MB): HBM and the launch; 24 us of which the first data
 //   take 3 (cold descriptors and pages) and the last epilogue 2.
 //   Small sizes: latency; about 3 us to the first data, 0.24 us per K-block, 2 us of epilogue.
@@ -92,7 +92,8 @@ struct DenseCfg {
 };
 
 // tile -> product p, m-tile, n-tile: inside a product, groups of 8 m-tiles with m fastest, so the
-// units running at one time share both operands' rows in L2.
+// units running at one time share both operands' rows in L2 (forward pass at T = 8192, d = 7168, F = 2048
+// over seconds: groups of 4, 8, 16, 32: 612, 608, 614, 629 us).
 __device__ __forceinline__ void dense_tile_at(const DenseArgs& a, int tile, int& p, int& m, int& n) {
   p = 0;
   while (p + 1 < a.n_problems && tile >= a.p[p + 1].tile0) ++p;
