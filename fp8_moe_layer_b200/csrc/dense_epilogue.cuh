@@ -7,10 +7,11 @@
 
 namespace moe {
 
-// sigmoid with the fast exponential and division; the exponent is clamped so that the denominator
-// stays finite (relative error ~1e-6, far below the 16-bit rounding that follows).
+// sigmoid with the fast exponential and division (relative error ~1e-6, far below the 16-bit rounding
+// that follows). Below -87.3 it is 0: the fast division gives 0 for denominators above 2^126 and for
+// infinity, so g s and its derivative vanish there for every finite g.
 __device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.f, 1.f + __expf(fminf(-x, 80.f)));
+  return __fdividef(1.f, 1.f + __expf(-x));
 }
 
 // f(g) = g s with s = sigmoid(g) (SiLU) or sigmoid(2 z), z = sqrt(2/pi) (g + 0.044715 g^3) (GELU,
@@ -21,7 +22,7 @@ __device__ __forceinline__ void gate_fn(int act, float g, float& f, float& df) {
   constexpr float kB = 0.044715f;
   float arg = g, slope = 1.f;
   if (act == kActGeluTanh) {
-    const float g2 = g * g;
+    const float g2 = fminf(g * g, 1e30f);            // (s is 0 or 1 long before: no infinity times 0)
     arg = kC * g * fmaf(kB, g2, 1.f);
     if (GRAD) slope = kC * fmaf(3.f * kB, g2, 1.f);
   }

@@ -466,6 +466,36 @@ def test_a_non_finite_token_stays_alone(ops, T):
     assert torch.equal(o[0][rest], o[1][rest]) and o[1][1:3].isnan().all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [6, 140])
+def test_saturated_gates(ops, act, T):
+    """Pre-activations far beyond where the gate saturates: f = f' = 0 below (as at -200, where both are
+    0 in fp32), f = g and f' = 1 above. Only the row's own gradients see them."""
+    x, w13, w2, dy = ffn_inputs(T, 64, 48, torch.bfloat16, 4)
+    x, h = x.clone(), ops.moe_gated_ffn(x, w13, w2, save_h=True)[1]
+    low = h.clone()
+    low[::2, :48] = -200.0
+    want = ops.moe_gated_ffn_backward(dy, x, w13, w2, low, activation=act)
+    for g in (-1e4, -1e12, -1e19, -3e38):
+        low[::2, :48] = g
+        for a, b in zip(ops.moe_gated_ffn_backward(dy, x, w13, w2, low, activation=act), want):
+            assert torch.equal(a, b), g
+    for g in (1e4, 1e12, 1e19, 1e30):
+        high = h.clone()
+        high[1, 5] = g
+        got = ops.moe_gated_ffn_backward(dy, x, w13, w2, high, activation=act)
+        for a, (ref, _) in zip(got, R.gated_ffn_backward(dy, x, w13, w2, high, act)):
+            # dh, act and the result are rounded to half a step each: below 2^-6 of the value's norm
+            assert float(torch.linalg.norm(a.double() - ref)) <= float(torch.linalg.norm(ref)) / 64, g
+    # and forward: a token whose gates reach -+1e30 and saturate
+    big = x.clone()
+    big[0] *= 1e30
+    y, gh = ops.moe_gated_ffn(big, w13, w2, activation=act, save_h=True)
+    a = torch.where(gh[:, :48].double() < 0, 0.0, gh[:, :48].double()) * gh[:, 48:].double()
+    assert bool((a[0].abs() > 1e30).any())
+    assert torch.equal(y[1:], ops.moe_gated_ffn(x, w13, w2, activation=act)[1:])
+
+
 def test_no_tokens(ops):
     dev = "cuda"
     x = torch.empty(0, 64, device=dev, dtype=torch.bfloat16)
