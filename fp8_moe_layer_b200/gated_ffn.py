@@ -11,6 +11,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import ops
@@ -37,10 +38,15 @@ class _GatedFFN(torch.autograd.Function):
 
 
 def gated_ffn(x, w13, w2, activation: str = "silu"):
-    """(act(x Wg^T) * (x Wu^T)) W2^T for x [..., d] in bf16 or fp16, with first-order gradients for
-    x, w13 [2F, d] and w2 [d, F]. The pre-activations are kept for the backward pass when one of
-    them asks for a gradient. (Capturing the backward pass into a CUDA graph follows torch's rule:
-    no eager graph of the same leaves may be alive during the capture.)"""
+    """(act(x Wg^T) * (x Wu^T)) W2^T for x [..., d] in bf16 or fp16, with first-order reverse-mode
+    gradients for x, w13 [2F, d] and w2 [d, F]; tensors that carry a forward-mode tangent are refused.
+    The pre-activations are kept for the backward pass when one of them asks for a gradient. (Capturing
+    the backward pass into a CUDA graph follows torch's rule: no eager graph of the same leaves may be
+    alive during the capture.)"""
+    # (a dual tensor need not require a gradient: without a word its tangent would come back as none,
+    # which stands for a derivative of zero)
+    if any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w13, w2)):
+        raise NotImplementedError("gated_ffn has no forward-mode derivative")
     rows = x.reshape(-1, x.shape[-1]).contiguous()
     # (asked here: inside the function torch reports the leaves' wishes under no_grad as well)
     if torch.is_grad_enabled() and any(t.requires_grad for t in (x, w13, w2)):

@@ -1,0 +1,52 @@
+"""What the gated FFN modules do around the library's calls, with the calls stubbed (no GPU)."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+
+@pytest.fixture(scope="module")
+def gffn():
+    from fp8_moe_layer_b200 import build
+    build.build()
+    from fp8_moe_layer_b200 import gated_ffn
+    return gated_ffn
+
+
+@pytest.fixture
+def stub(gffn, monkeypatch):
+    """The library's forward call as torch operations that, like it, leave no derivative behind."""
+    def forward(x, w13, w2, activation="silu", save_h=False, ws=None):
+        with torch.no_grad(), forward_ad._set_fwd_grad_enabled(False):
+            h = x @ w13.t()
+            y = (torch.nn.functional.silu(h[:, :w2.shape[1]]) * h[:, w2.shape[1]:]) @ w2.t()
+        return (y, h) if save_h else y
+    monkeypatch.setattr(gffn.ops, "moe_gated_ffn", forward)
+
+
+def weights(d=16, F=32):
+    g = torch.Generator().manual_seed(0)
+    return [torch.randn(*n, generator=g) for n in ((3, d), (2 * F, d), (d, F))]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("grad", ["frozen", "leaf", "no_grad"])
+def test_forward_mode_tangents_are_refused(gffn, stub, which, grad):
+    """A dual tensor requires no gradient, so nothing but its tangent says that one is wanted."""
+    args = weights()
+    with forward_ad.dual_level():
+        dual = list(args)
+        dual[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        if grad == "leaf":
+            dual[(which + 1) % 3] = args[(which + 1) % 3].clone().requires_grad_()
+        with torch.set_grad_enabled(grad != "no_grad"), pytest.raises(NotImplementedError):
+            gffn.gated_ffn(*dual)
+        assert gffn.gated_ffn(*args).shape == (3, 16)        # plain tensors inside a dual level
+    with pytest.raises((NotImplementedError, RuntimeError)):
+        torch.func.jvp(lambda t: gffn.gated_ffn(t, *args[1:]), (args[0],), (args[0],))
+
+
+def test_module_refuses_forward_mode_tangents(gffn, stub):
+    ffn = gffn.GatedFFN(16, 32, dtype=torch.float32, device="cpu").requires_grad_(False)
+    x = weights()[0]
+    with forward_ad.dual_level(), pytest.raises(NotImplementedError):
+        ffn(forward_ad.make_dual(x, x))
