@@ -85,7 +85,8 @@ class GatedFFN(torch.nn.Module):
 
 
 class Int8GatedFFN:
-    """A W8A8 int8 SwiGLU FFN: codes w13 [2F, d], w2 [d, F] with scales [2F], [d]; bf16 tokens."""
+    """A W8A8 int8 SwiGLU FFN: codes w13 [2F, d], w2 [d, F] with scales [2F], [d]; bf16 tokens. It
+    serves: tokens whose gradient is wanted are refused."""
 
     def __init__(self, w13, w13_scale, w2, w2_scale):
         self.weights = tuple(t.unsqueeze(0) for t in (w13, w13_scale, w2, w2_scale))
@@ -93,6 +94,7 @@ class Int8GatedFFN:
 
     def __call__(self, x, dtype=torch.bfloat16):
         """y [..., d] of x [..., d] bf16, summed in fp32 and rounded once to ``dtype``."""
+        ops._no_derivative("Int8GatedFFN", x)
         rows = x.reshape(-1, x.shape[-1]).contiguous()
         T = rows.shape[0]
         offsets = torch.arange(2, dtype=torch.int32, device=x.device) * T     # one expert's rows

@@ -13,6 +13,7 @@ import os
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8moe.so")
@@ -393,6 +394,16 @@ def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
 
 
+def _no_derivative(where: str, x: torch.Tensor) -> None:
+    """Refuses an input whose derivative is wanted: a result without a graph would pass for one that
+    does not depend on it."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{where} has no backward pass: detach its input, or call it under "
+                           "torch.no_grad()")
+    if forward_ad.unpack_dual(x).tangent is not None:
+        raise NotImplementedError(f"{where} has no forward-mode derivative")
+
+
 def _workspace(ws: Optional[torch.Tensor], need: int, where: str, device) -> torch.Tensor:
     """The caller's workspace, or one from torch's allocator (reused in stream order)."""
     if need == 0:
@@ -554,7 +565,8 @@ class MoELayerInt8:
 
     router_w [E, d] and router_bias [E] (or None) fp32; w13 [E, 2F, d], w2 [E, d, F] int8 with scales
     [E, 2F], [E, d]; shared = (w13 [2F, d], scale [2F], w2 [d, F], scale [d]) or None, an always-on
-    expert of weight 1. Each call takes its own workspace from torch's allocator, so calls of one layer
+    expert of weight 1. The weights are constants, and hidden states whose gradient is wanted are
+    refused. Each call takes its own workspace from torch's allocator, so calls of one layer
     may be captured or run on several streams; ``ws`` is the last call's (for ``device_status``)."""
 
     def __init__(self, router_w, router_bias, k, k_max, w13, w13_scale, w2, w2_scale, shared=None):
@@ -589,6 +601,7 @@ class MoELayerInt8:
             raise ValueError("hidden must be [T, d]")
         T, dev = hidden.shape[0], self.router_w.device
         _expect("hidden", hidden, torch.bfloat16, (T, self.d), dev)
+        _no_derivative("MoELayerInt8", hidden)
         if k_per_token is not None:
             _expect("k_per_token", k_per_token, torch.int32, (T,), dev)
         k = self.k if k is None else int(k)

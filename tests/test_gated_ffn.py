@@ -50,3 +50,44 @@ def test_module_refuses_forward_mode_tangents(gffn, stub):
     x = weights()[0]
     with forward_ad.dual_level(), pytest.raises(NotImplementedError):
         ffn(forward_ad.make_dual(x, x))
+
+
+# ------------------------------------------------------------------------------ int8 layers
+def int8_weights(E, d, F):
+    return (torch.zeros(E, 2 * F, d, dtype=torch.int8), torch.ones(E, 2 * F),
+            torch.zeros(E, d, F, dtype=torch.int8), torch.ones(E, d))
+
+
+@pytest.fixture(params=["layer", "block"])
+def int8_call(gffn, monkeypatch, request):
+    """An int8 layer on the CPU, its library calls stubbed; it records the workspaces it was given."""
+    ops = gffn.ops
+    monkeypatch.setattr(ops, "_elsewhere", lambda device: False)
+    monkeypatch.setattr(ops, "alloc_workspace",
+                        lambda dm, device=None: torch.zeros(256, dtype=torch.uint8))
+    monkeypatch.setattr(ops, "moe_route_topk", lambda hidden, *a, **k: (
+        torch.zeros(hidden.shape[0], 2, dtype=torch.int32), torch.ones(hidden.shape[0], 2)))
+    monkeypatch.setattr(ops, "moe_permute", lambda *a, **k: (None, None, None))
+    monkeypatch.setattr(ops, "moe_grouped_ffn_int8",
+                        lambda hidden, *a, **k: torch.ones(hidden.shape))
+    monkeypatch.setattr(ops, "moe_combine", lambda out, *a, **k: out.bfloat16())
+    q = int8_weights(3, 64, 32)
+    if request.param == "layer":
+        return ops.MoELayerInt8(torch.zeros(3, 64), None, 2, 2, *q)
+    return gffn.Int8GatedFFN(*(t[0] for t in q))
+
+
+def test_int8_layers_refuse_inputs_whose_derivative_is_wanted(int8_call):
+    """They return a tensor without a graph: the layers below would get no gradient, without a word."""
+    x = torch.ones(5, 64, dtype=torch.bfloat16)
+    leaf = x.clone().requires_grad_()
+    for t in (leaf, leaf * 2):
+        with pytest.raises(RuntimeError):
+            int8_call(t)
+        with torch.no_grad():
+            assert int8_call(t).shape == (5, 64)
+        assert int8_call(t.detach()).shape == (5, 64)
+    with torch.inference_mode():
+        assert int8_call(leaf).shape == (5, 64)
+    with forward_ad.dual_level(), torch.no_grad(), pytest.raises(NotImplementedError):
+        int8_call(forward_ad.make_dual(x, x))
