@@ -132,10 +132,12 @@ def workspace_bytes(dm: MoEDims) -> int:
     return int(LIB.moe_workspace_bytes(ctypes.byref(dm)))
 
 
-def alloc_workspace(dm: MoEDims, device=None) -> torch.Tensor:
-    """Workspace for every entry point with these dims, its status word cleared."""
-    n = workspace_bytes(dm)
-    if n == 0:
+def alloc_workspace(dm: MoEDims, device=None, also: Optional[MoEDims] = None) -> torch.Tensor:
+    """Workspace for every entry point with these dims (and, one after the other, with those of
+    ``also``), its status word cleared."""
+    need = [workspace_bytes(m) for m in (dm, also) if m is not None]
+    n = max(need)
+    if min(need) == 0:
         raise MoEError(MOE_ERR_INVALID_ARG, "workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     _check(LIB.moe_clear_status(ws.data_ptr(), _stream(ws.device)), "moe_clear_status")
@@ -612,7 +614,11 @@ class MoELayerInt8:
         if _elsewhere(dev):
             with torch.cuda.device(dev):
                 return self(hidden, k_per_token, k)
-        self.ws = ws = alloc_workspace(dims(T, self.d, self.E, self.F, self.k_max), dev)
+        # one workspace for the routed and the shared experts, so that its status word has the failures
+        # of both; the last call's goes back to torch's allocator first
+        also = None if self.shared is None else dims(T, self.d, 1, self.shared[2].shape[2], 1)
+        self.ws = None
+        self.ws = ws = alloc_workspace(dims(T, self.d, self.E, self.F, self.k_max), dev, also)
         ids, w = moe_route_topk(hidden, self.router_w, self.router_bias, k, k_per_token,
                                 self.k_max, F=self.F, ws=ws)
         offsets, perm, inv = moe_permute(ids, k, k_per_token, self.E, d=self.d, F=self.F, ws=ws)
@@ -621,5 +627,5 @@ class MoELayerInt8:
         if self.shared is not None:
             one = torch.arange(2, dtype=torch.int32, device=dev) * T         # one expert's rows
             shared_out = moe_grouped_ffn_int8(
-                hidden, *self.shared, one, torch.arange(T, dtype=torch.int32, device=dev), 1)
+                hidden, *self.shared, one, torch.arange(T, dtype=torch.int32, device=dev), 1, ws=ws)
         return moe_combine(out, w, inv, shared_out=shared_out)

@@ -60,11 +60,11 @@ def int8_weights(E, d, F):
 
 @pytest.fixture(params=["layer", "block"])
 def int8_call(gffn, monkeypatch, request):
-    """An int8 layer on the CPU, its library calls stubbed; it records the workspaces it was given."""
+    """An int8 layer on the CPU, its library calls stubbed."""
     ops = gffn.ops
     monkeypatch.setattr(ops, "_elsewhere", lambda device: False)
     monkeypatch.setattr(ops, "alloc_workspace",
-                        lambda dm, device=None: torch.zeros(256, dtype=torch.uint8))
+                        lambda *a, **k: torch.zeros(256, dtype=torch.uint8))
     monkeypatch.setattr(ops, "moe_route_topk", lambda hidden, *a, **k: (
         torch.zeros(hidden.shape[0], 2, dtype=torch.int32), torch.ones(hidden.shape[0], 2)))
     monkeypatch.setattr(ops, "moe_permute", lambda *a, **k: (None, None, None))

@@ -1,0 +1,76 @@
+"""Failures on the device that the host cannot see, and where a user finds them.
+
+The wait-test build of the library (include/moe_testing.h) bounds every wait inside a kernel at 2 ms and
+can withhold one signal of the gate/up GEMM; nothing here faults, traps or hangs the GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from tests.test_gpu_operators import gen, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from fp8_moe_layer_b200 import ops
+    return ops
+
+
+@pytest.fixture(scope="module")
+def waittest(ops):
+    from fp8_moe_layer_b200 import build
+    lib = ops.load_library(build.build(lib=build.LIB_WAITTEST))
+    lib.moe_test_withhold_gemm_commit.argtypes = [ctypes.c_int]
+    lib.moe_test_withhold_gemm_commit.restype = None
+    yield lib
+    lib.moe_test_withhold_gemm_commit(0)
+
+
+def int8_layer(ops, T=40, d=144, F=80, E=4):
+    g = gen(T)
+    layer = ops.MoELayerInt8.from_weights(
+        rnd(g, E, d) * 0.05, None, 2, 2, rnd(g, E, 2 * F, d) / d ** 0.5, rnd(g, E, d, F) / F ** 0.5,
+        shared=(rnd(g, 2 * F, d) / d ** 0.5, rnd(g, d, F) / F ** 0.5))
+    return layer, rnd(g, T, d).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("late", ["routed", "shared"])
+def test_either_chain_of_the_int8_layer_reports_to_its_workspace(ops, waittest, monkeypatch, late):
+    """A wait that runs out in the shared expert's launches alone, or in the routed ones alone."""
+    layer, x = int8_layer(ops)
+    want = layer(x)
+    assert ops.device_status(layer.ws) == ops.MOE_OK
+    monkeypatch.setattr(ops, "LIB", waittest)
+    real, calls = ops.moe_grouped_ffn_int8, []
+
+    def grouped(*args, **kw):
+        calls.append(args[1].shape[0])
+        waittest.moe_test_withhold_gemm_commit(int((len(calls) == 2) == (late == "shared")))
+        try:
+            return real(*args, **kw)
+        finally:
+            waittest.moe_test_withhold_gemm_commit(0)
+
+    monkeypatch.setattr(ops, "moe_grouped_ffn_int8", grouped)
+    layer(x)
+    assert calls == [4, 1]
+    assert ops.device_status(layer.ws) == ops.MOE_ERR_DEVICE_TIMEOUT
+    monkeypatch.undo()
+    assert torch.equal(layer(x), want)                       # the context and the layer go on
+    assert ops.device_status(layer.ws) == ops.MOE_OK
+
+
+def test_int8_layer_gives_its_last_workspace_back_first(ops):
+    """A call takes no second workspace while the last call's is still held."""
+    layer, x = int8_layer(ops, T=4000, d=1024, F=512)
+    layer(x)
+    held = layer.ws.numel()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    layer(x)
+    assert layer.ws.numel() == held
+    assert torch.cuda.max_memory_allocated() - before < held
