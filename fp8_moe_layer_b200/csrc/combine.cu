@@ -189,17 +189,19 @@ __global__ void __launch_bounds__(256) combine_kernel(
   }
 }
 
-// out[r, :] = sum_s o[s][r, :] for r < R (split entry point with a K-split down GEMM).
+// out[r, :] = sum_s o[s][r, :] for offsets[0] <= r < offsets[E] (split entry points with a K-split down
+// GEMM). Nothing is written after offsets that were found inconsistent (an empty tile list): no GEMM ran.
 __global__ void __launch_bounds__(256) reduce_splits_kernel(const float* __restrict__ o, int splits,
                                                             size_t split_stride,
-                                                            const int32_t* __restrict__ total_rows,
+                                                            const int32_t* __restrict__ offsets,
+                                                            const int32_t* __restrict__ tiles, int E,
                                                             int64_t rcap, int d,
                                                             float* __restrict__ out) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
-  const int R = (int)min((int64_t)max(*total_rows, 0), rcap);
+  const int R0 = max(offsets[0], 0), R = tiles[E] > 0 ? (int)min((int64_t)offsets[E], rcap) : 0;
   const int nv = d / 4;
-  for (int r = blockIdx.x; r < R; r += gridDim.x) {
+  for (int r = R0 + blockIdx.x; r < R; r += gridDim.x) {
     for (int i = threadIdx.x; i < nv; i += blockDim.x) {
       float4 v = reinterpret_cast<const float4*>(o + (size_t)r * d)[i];
       for (int s = 1; s < splits; ++s) {
@@ -251,9 +253,10 @@ cudaError_t launch_combine(const Plan& p, const float* o, int splits, size_t spl
 }
 
 cudaError_t launch_reduce_splits(const Plan& p, const float* o, int splits, size_t split_stride,
-                                 const int32_t* total_rows, float* out, cudaStream_t s) {
-  launch_pdl(reduce_splits_kernel, dim3(row_grid(p.Rcap)), dim3(256), 0, s, o, splits, split_stride, total_rows,
-                                                        p.Rcap, p.d, out);
+                                 const int32_t* offsets, const int32_t* tiles, float* out,
+                                 cudaStream_t s) {
+  launch_pdl(reduce_splits_kernel, dim3(row_grid(p.Rcap)), dim3(256), 0, s, o, splits, split_stride,
+             offsets, tiles, p.E, p.Rcap, p.d, out);
   return cudaGetLastError();
 }
 

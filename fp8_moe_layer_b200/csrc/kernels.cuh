@@ -171,7 +171,8 @@ cudaError_t launch_combine(const Plan& p, const float* o, int splits, size_t spl
                            const int32_t* shared_row0, int shared_splits, uint16_t* y,
                            float* y_f32, cudaStream_t s);
 cudaError_t launch_reduce_splits(const Plan& p, const float* o, int splits, size_t split_stride,
-                                 const int32_t* total_rows, float* out, cudaStream_t s);
+                                 const int32_t* offsets, const int32_t* tiles, float* out,
+                                 cudaStream_t s);
 
 // Expert-parallel dispatch over n_ranks contiguous expert blocks: plan (send rows in (rank,
 // token) order, local ids and weights, per-rank counts, the combine map) and the row gather.

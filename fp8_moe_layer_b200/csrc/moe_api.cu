@@ -536,7 +536,7 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
   MOE_TRY(run_ffn(q, w, w13, w13_scale, w2, w2_scale, nullptr, nullptr, nullptr, nullptr,
                   direct ? expert_out : w.o, (size_t)p.Rpad * p.d, q.Rcap, nullptr, s, int8));
   if (!direct)
-    MOE_CUDA(launch_reduce_splits(q, w.o, p.g2_splits, (size_t)p.Rpad * p.d, w.offsets + p.E,
+    MOE_CUDA(launch_reduce_splits(q, w.o, p.g2_splits, (size_t)p.Rpad * p.d, w.offsets, w.tiles,
                                   expert_out, s));
   return MOE_OK;
 }

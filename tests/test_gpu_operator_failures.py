@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from tests.test_gpu_operators import gen, rnd
+from tests.test_gpu_operators import int8_layer as operands
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,24 @@ def test_int8_layer_gives_its_last_workspace_back_first(ops):
     layer(x)
     assert layer.ws.numel() == held
     assert torch.cuda.max_memory_allocated() - before < held
+
+
+# ------------------------------------------------------------------------------ routing data out of range
+def poisoned_workspace(ops, *sizes):
+    """A workspace whose bytes read as 3.0 behind the status block: what an earlier call may have left."""
+    ws = ops.alloc_workspace(ops.dims(*sizes))
+    ws[256:] = 0x40
+    return ws
+
+
+def test_fp8_experts_write_nothing_for_bad_offsets(ops):
+    """With the down product's K split: its partial sums are not read where no product ran."""
+    T, d, E, F, k = 2, 64, 4, 8208, 2
+    hid, ids, _, _, s13, _, s2 = operands(T, d, E, F, k, 3)
+    off, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    w13 = torch.full((E, 2 * F, d), 0x38, dtype=torch.uint8, device="cuda")      # e4m3 one
+    w2 = torch.full((E, d, F), 0x38, dtype=torch.uint8, device="cuda")
+    off[2] = off[3] + 1
+    ws = poisoned_workspace(ops, T, d, E, F, k)
+    out = ops.moe_grouped_ffn_fp8(hid, w13, s13, w2, s2, off, perm, k, ws=ws)
+    assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_CHECK and (out == 0).all()
