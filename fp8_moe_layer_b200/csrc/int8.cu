@@ -62,7 +62,8 @@ cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8
 
 // Everything the routed int8 FFN needs before its first GEMM, in one launch: block 0 checks the
 // caller's offsets and writes the GEMMs' tile prefix; the others fill the routed rows, clear each row's
-// SwiGLU maximum and zero the output rows behind the last routed one. For few rows a block quantises
+// SwiGLU maximum and zero the output rows of no expert, before the first routed one and behind the last.
+// Offsets that are out of order zero the whole output. For few rows a block quantises
 // hidden[perm[r]] straight into row r (no launch for the tokens' codes). For many (COPY), quantising a
 // token once and copying its codes by a warp per row is cheaper than quantising it k times: Qwen3
 // shape, T = 4096, k = 8: 51 us for the latter. An index outside [0, T) gives a zero row and flags
@@ -95,6 +96,10 @@ __global__ void __launch_bounds__(256) int8_prepare_kernel(const Int8Prepare a) 
     for (int w = 0; w < warp; ++w) at += sums[w];
     if (bad) {                                     // an empty tile list: no GEMM work is done
       for (int e = tid; e <= a.E; e += 256) a.tiles[e] = 0;
+      // and the whole output is zero (the other blocks, which do not know, leave some of its rows)
+      const int64_t n = a.rcap * a.d / 4;
+      for (int64_t i = tid; i < n; i += 256)
+        reinterpret_cast<float4*>(a.out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (tid == 0) report(a.status, kStatusDeviceCheck, kWhereTilePrefix, 0);
       return;
     }
@@ -106,10 +111,11 @@ __global__ void __launch_bounds__(256) int8_prepare_kernel(const Int8Prepare a) 
     return;
   }
   const int R = (int)min((int64_t)max(a.offsets[a.E], 0), a.rcap);
+  const int R0 = min(max(a.offsets[0], 0), R);     // (rows before the first expert's)
   const int me = COPY ? lane : tid, step = COPY ? 32 : 256;
   const int64_t first = COPY ? (int64_t)(blockIdx.x - 1) * 8 + warp : blockIdx.x - 1;
   for (int64_t r = first; r < a.rcap; r += (COPY ? 8 : 1) * (int64_t)(gridDim.x - 1)) {
-    if (r >= R) {
+    if (r >= R || r < R0) {
       float4* o = reinterpret_cast<float4*>(a.out + (size_t)r * a.d);
       for (int i = me; i < a.d / 4; i += step) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;

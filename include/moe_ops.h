@@ -58,9 +58,11 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
  *   act[f] = silu(h[f]) * h[F+f] (fp32);  s2, aq = quantised act over all F;
  *   expert_out[r,i] = s2 * w2_scale[e,i] * sum_f aq[f] * w2[e,i,f]
  *   w13 [E, 2F, d] int8; w2 [E, d, F] int8; every other argument, the layouts, the workspace
- *   (moe_workspace_bytes) and the errors as for moe_grouped_ffn_fp8, with rows >= R of expert_out
- *   set to zero; like it, this entry point leaves the status word as it is. expert_offsets must not
- *   be overwritten before the call has run. d and F at most 131056. */
+ *   (moe_workspace_bytes) and the errors as for moe_grouped_ffn_fp8; like it, this entry point leaves
+ *   the status word as it is. Every row of expert_out is written: rows of no expert (r >= R, or
+ *   r < expert_offsets[0]) and rows whose token index is out of range are zero, and so is all of it
+ *   where the offsets flag MOE_ERR_DEVICE_CHECK. expert_offsets must not be overwritten before the
+ *   call has run. d and F at most 131056. */
 int moe_grouped_ffn_int8(const moe_dims* dims, const uint16_t* hidden, const int8_t* w13,
                          const float* w13_scale, const int8_t* w2, const float* w2_scale,
                          const int32_t* expert_offsets, const int32_t* perm_token,

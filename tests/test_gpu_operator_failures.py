@@ -7,6 +7,7 @@ import ctypes
 import pytest
 import torch
 
+from tests import operator_refs as R
 from tests.test_gpu_operators import gen, rnd
 from tests.test_gpu_operators import int8_layer as operands
 
@@ -78,11 +79,61 @@ def test_int8_layer_gives_its_last_workspace_back_first(ops):
 
 
 # ------------------------------------------------------------------------------ routing data out of range
+# a few rows; the down product's K split; many rows (a token's codes are copied); 256-row token tiles
+ROUTED = [(9, 144, 4, 80, 2), (2, 64, 4, 8208, 2), (700, 144, 64, 80, 2), (900, 144, 3, 80, 2)]
+
+
 def poisoned_workspace(ops, *sizes):
     """A workspace whose bytes read as 3.0 behind the status block: what an earlier call may have left."""
     ws = ops.alloc_workspace(ops.dims(*sizes))
     ws[256:] = 0x40
     return ws
+
+
+@pytest.mark.parametrize("T,d,E,F,k", ROUTED)
+@pytest.mark.parametrize("bad", ["order", "count", "negative", "token"])
+def test_int8_experts_write_every_row_for_bad_routing_data(ops, T, d, E, F, k, bad):
+    hid, ids, _, q13, s13, q2, s2 = operands(T, d, E, F, k, 1)
+    off, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    good = ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, perm, k)
+    o, p = off.clone(), perm.clone()
+    if bad == "order":
+        o[2] = o[3] + 1
+    elif bad == "count":
+        o[E] = T * k + 1
+    elif bad == "negative":
+        o[0] = -1
+    else:
+        p[1], p[3] = T + 5, -1
+    ws = poisoned_workspace(ops, T, d, E, F, k)
+    held = torch.full((T * k, d), 3.0, device="cuda")        # where the output is likely to go
+    del held
+    out = ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, o, p, k, ws=ws)
+    assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_CHECK
+    if bad == "token":
+        good[[1, 3]] = 0
+        assert torch.equal(out, good)
+    else:
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("T,d,E,F,k", ROUTED)
+def test_int8_experts_behind_the_first_ones(ops, T, d, E, F, k):
+    """Offsets that start behind row 0 (the rows of experts held elsewhere): those rows are zero."""
+    hid, ids, _, q13, s13, q2, s2 = operands(T, d, E, F, k, 2)
+    ids = (torch.arange(T, device="cuda")[:, None] + torch.arange(k, device="cuda")).int() % E
+    off, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    first = 2
+    ws = poisoned_workspace(ops, T, d, E - first, F, k)
+    out = ops.moe_grouped_ffn_int8(hid, *(t[first:].contiguous() for t in (q13, s13, q2, s2)),
+                                   off[first:].clone(), perm, k, ws=ws)
+    assert ops.device_status(ws) == ops.MOE_OK
+    ends = off.tolist()
+    assert 0 < ends[first] < T * k and (out[:ends[first]] == 0).all()
+    for e in range(first, E):
+        rows = slice(ends[e], ends[e + 1])
+        if ends[e] < ends[e + 1]:
+            R.check(out[rows], R.expert_int8(hid[perm[rows].long()], q13[e], s13[e], q2[e], s2[e]), e)
 
 
 def test_fp8_experts_write_nothing_for_bad_offsets(ops):
