@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kPermThreads) tile_prefix_kernel(
   __syncthreads();
   if (bad) {
     // inconsistent offsets: publish an empty tile list so no GEMM work is done
-    if (e <= E) tiles[e] = 0;
+    for (int i = e; i <= E; i += blockDim.x) tiles[i] = 0;   // (E may be the block's size)
     if (threadIdx.x == 0) report(status, kStatusDeviceCheck, kWhereTilePrefix, 0);
     return;
   }

@@ -147,3 +147,20 @@ def test_fp8_experts_write_nothing_for_bad_offsets(ops):
     ws = poisoned_workspace(ops, T, d, E, F, k)
     out = ops.moe_grouped_ffn_fp8(hid, w13, s13, w2, s2, off, perm, k, ws=ws)
     assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_CHECK and (out == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+def test_bad_offsets_of_the_largest_expert_count(ops, fmt):
+    """1024 experts are as many as the tile prefix has threads: its last entry, the number of tiles, is
+    one more."""
+    T, d, E, F, k = 4, 16, 1024, 16, 2
+    hid, ids, _, q13, s13, q2, s2 = operands(T, d, E, F, k, 4)
+    off, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    off[7] = off[8] + 1
+    ws = poisoned_workspace(ops, T, d, E, F, k)
+    if fmt == "fp8":
+        out = ops.moe_grouped_ffn_fp8(hid, q13.view(torch.uint8), s13, q2.view(torch.uint8), s2, off, perm,
+                                      k, ws=ws)
+    else:
+        out = ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, perm, k, ws=ws)
+    assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_CHECK and (out == 0).all()
