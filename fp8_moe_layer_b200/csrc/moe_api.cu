@@ -206,9 +206,17 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
     es[i] = 1;
     if (i + 1 < rank) gs[i] = strides[i];
   }
-  return fn(m, dtype, rank, const_cast<void*>(base), gd, gs, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(m, dtype, rank, const_cast<void*>(base), gd, gs, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // The encoder is a driver call and needs a current context. A thread gets the device's from its first
+  // runtime call that needs one, which this may come before: a worker thread, or autograd's, whose
+  // tensors all came from an allocator's cache. Setting the current device makes its context current.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 // fp32 down-GEMM output [rows][d] (all K-split partials stacked): box 32 channels x 32 rows,
