@@ -23,7 +23,7 @@ LIB_ROLES = os.path.join(HERE, "libfp8moe_roles.so")
 VARIANTS = {LIB: [], LIB_WAITTEST: ["-DMOE_WAIT_TEST"], LIB_ROLES: ["-DMOE_ROLE_COUNTERS"]}
 SOURCES = ["moe_api.cu", "route.cu", "router_mma.cu", "permute.cu", "gemm.cu", "combine.cu",
            "noalloc.cu", "dispatch.cu", "dense_gemm.cu", "few_rows.cu",
-           "int8.cu", "gated_ffn.cu"]
+           "int8.cu", "gated_ffn.cu", "failures.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

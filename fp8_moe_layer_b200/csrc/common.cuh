@@ -31,12 +31,24 @@ enum Where : int {
   kWhereGemm2 = 6, kWhereCombine = 7, kWhereTilePrefix = 8, kWhereDispatch = 9, kWhereDense = 10,
 };
 
-__device__ __forceinline__ void report(int* status, int code, int where, int detail) {
-  if (status == nullptr) return;
-  if (atomicCAS(status, 0, code) == 0) {
-    atomicExch(status + 1, where);
-    atomicExch(status + 2, detail);
+// The first failure that a kernel of this translation unit reported on a device, {code, where, detail}:
+// it outlives the workspaces (include/moe_failures.h). Device code of one translation unit cannot see
+// another's variables here (no relocatable device code), so each has its own, listed on the host.
+static __device__ int g_failure[4];
+struct FailureWord {
+  explicit FailureWord(const void* symbol);          // (failures.cu; runs while the library is loaded)
+};
+static const FailureWord g_failure_word(g_failure);
+
+__device__ __forceinline__ void record(int* word, int code, int where, int detail) {
+  if (atomicCAS(word, 0, code) == 0) {
+    atomicExch(word + 1, where);
+    atomicExch(word + 2, detail);
   }
+}
+__device__ __forceinline__ void report(int* status, int code, int where, int detail) {
+  record(g_failure, code, where, detail);
+  if (status != nullptr) record(status, code, where, detail);
 }
 
 // Upper bound of every spin-wait: ~1 s of %globaltimer, and an iteration cap as a second bound.

@@ -59,6 +59,9 @@ struct DenseArgs {
   int E;
   float* out32;
   uint32_t* row_amax;
+#ifdef MOE_WAIT_TEST
+  int withhold;                  // skip the first tile's accumulator signal
+#endif
 };
 
 // Tile of a launch: 256 x 256 on a 2-CTA pair, or 128 x bn on one CTA, its K split over `split` CTAs;

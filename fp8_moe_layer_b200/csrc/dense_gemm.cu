@@ -596,7 +596,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             phase ^= 1u;
           }
         }
-        if (ok) {
+        bool signal = ok;
+#ifdef MOE_WAIT_TEST
+        if (args.withhold && tile == unit) signal = false;   // the epilogue's wait will expire
+#endif
+        if (signal) {                                // accumulators ready for the epilogue(s)
           if constexpr (PAIR) {
             mma_commit_pair(tfull_l + 8u * buf);
             mma_commit_pair(tfull_p + 8u * buf);

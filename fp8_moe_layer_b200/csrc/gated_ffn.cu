@@ -99,6 +99,9 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
     a.act = dims->act;
     a.clear_status = 1;
     a.save_h = h != nullptr;
+#ifdef MOE_WAIT_TEST
+    a.withhold = g_withhold_gemm_commit;
+#endif
     a.status = status;
     DenseProblem& g = a.p[0];
     g.M = T;
@@ -177,6 +180,9 @@ int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const u
   a.type = type;
   a.act = dims->act;
   a.h = h;
+#ifdef MOE_WAIT_TEST
+  a.withhold = g_withhold_gemm_commit;
+#endif
   a.status = status;
   a.clear_status = 1;
   DenseProblem& g = a.p[0];                        // dL/da = dy W2: W2 [d, F] as it lies

@@ -1,5 +1,5 @@
-"""Python binding of the library's C ABI (``include/moe.h`` and ``include/moe_ops.h``), through
-ctypes.
+"""Python binding of the library's C ABI (``include/moe.h``, ``include/moe_ops.h`` and
+``include/moe_failures.h``), through ctypes.
 
 Argument marshalling only: every step of the layer runs in the CUDA library ``libfp8moe.so``.
 Importing this module loads that library and raises if it has not been built; there is no other
@@ -80,6 +80,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_forward": (ctypes.c_int, [dims_p, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                        vp, vp, vp, sz, vp, ctypes.POINTER(MoEDebugOut)]),
         "moe_route_topk_noalloc": (ctypes.c_int, [dims_p, vp, vp, vp, i32, vp, vp, vp, vp]),
+        "moe_device_failure": (ctypes.c_int, [i32, vp, vp]),
         "moe_kernel_launch_count": (ctypes.c_uint64, []),
         "moe_ep_dispatch": (ctypes.c_int, [dims_p, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                            vp, vp, sz, vp]),
@@ -191,6 +192,20 @@ def device_status(ws: torch.Tensor) -> int:
 
 def clear_status(ws: torch.Tensor) -> None:
     _check(LIB.moe_clear_status(ws.data_ptr(), _stream(ws.device)), "moe_clear_status")
+
+
+def device_failure(device=None, clear: bool = True) -> int:
+    """The first failure that any kernel of the library recorded on ``device`` (default: the current
+    one) since this was last asked, whichever workspace it went to: MOE_OK or a MOE_ERR_DEVICE_* code.
+
+    A bounded wait that expired leaves its call's outputs incomplete. ``device_status`` says so for a
+    workspace that its caller holds; this also covers the calls that take a workspace of their own
+    (``ws=None``, ``gated_ffn`` and its backward pass, ``Int8GatedFFN``, replays of graphs). It waits
+    for the current stream: ask once per step or batch, not per call, and not while capturing."""
+    out = (ctypes.c_int32 * 3)()
+    with torch.cuda.device(device):
+        _check(LIB.moe_device_failure(int(clear), out, _stream()), "moe_device_failure")
+    return int(out[0])
 
 
 # ------------------------------------------------------------------------------ entry points

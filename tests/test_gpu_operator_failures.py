@@ -164,3 +164,73 @@ def test_bad_offsets_of_the_largest_expert_count(ops, fmt):
     else:
         out = ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, perm, k, ws=ws)
     assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_CHECK and (out == 0).all()
+
+
+# ------------------------------------------------------------------------------ workspaces that nobody keeps
+def kept_failure(ops):
+    """(what is kept on the device, what is left after asking for it)."""
+    return ops.device_failure(), ops.device_failure()
+
+
+def failing(lib, call):
+    lib.moe_test_withhold_gemm_commit(1)
+    try:
+        return call()
+    finally:
+        lib.moe_test_withhold_gemm_commit(0)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("which", ["forward", "function", "backward", "int8 block", "replay"])
+def test_a_failure_outlives_its_workspace(ops, waittest, monkeypatch, which, T):
+    """A wait that runs out in a call whose workspace is gone when it returns."""
+    from fp8_moe_layer_b200.gated_ffn import GatedFFN, gated_ffn
+    torch.manual_seed(0)
+    monkeypatch.setattr(ops, "LIB", waittest)
+    ffn = GatedFFN(144, 80)
+    x = torch.randn(T, 144, device="cuda").to(torch.bfloat16)
+    served, plain = ffn.to_int8(), ffn.w13.detach()
+    want = ffn(x)
+    ops.device_failure()
+    assert kept_failure(ops) == (ops.MOE_OK, ops.MOE_OK)
+    if which == "forward":
+        failing(waittest, lambda: ffn(x))
+    elif which == "function":
+        failing(waittest, lambda: gated_ffn(x, plain, ffn.w2.detach()))
+    elif which == "backward":
+        failing(waittest, lambda: want.backward(want.detach()))
+    elif which == "int8 block":
+        failing(waittest, lambda: served(x))
+    else:
+        s = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.no_grad(), torch.cuda.graph(graph, stream=s):
+            failing(waittest, lambda: ffn(x))
+        assert kept_failure(ops) == (ops.MOE_OK, ops.MOE_OK)
+        graph.replay()
+    assert kept_failure(ops) == (ops.MOE_ERR_DEVICE_TIMEOUT, ops.MOE_OK)
+    with torch.no_grad():
+        assert torch.equal(ffn(x), want)                     # and the calls that follow are whole
+    assert kept_failure(ops) == (ops.MOE_OK, ops.MOE_OK)
+
+
+def test_failures_of_every_kernel_file_are_kept(ops):
+    """Caller data out of range, as found by the grouping, the preparations and the combine."""
+    T, d, E, F, k = 9, 144, 4, 80, 2
+    hid, ids, w, q13, s13, q2, s2 = operands(T, d, E, F, k, 1)
+    off, perm, inv = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    out = ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, perm, k)
+    ops.device_failure()
+    wrong_id, wrong_token, wrong_row = ids.clone(), perm.clone(), inv.clone()
+    wrong_id[0, 0], wrong_token[0], wrong_row[0, 0] = E + 2, T + 2, T * k + 2
+    u13, u2 = q13.view(torch.uint8), q2.view(torch.uint8)
+    for call in (lambda: ops.moe_permute(wrong_id, k, None, E, d=d, F=F),
+                 lambda: ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, wrong_token, k),
+                 lambda: ops.moe_grouped_ffn_fp8(hid, u13, s13, u2, s2, off, wrong_token, k),
+                 lambda: ops.moe_combine(out, w, wrong_row),
+                 lambda: ops.moe_route_topk(hid, torch.zeros(E, d, device="cuda"), None, k,
+                                            torch.full((T,), k + 3, device="cuda", dtype=torch.int32), k),
+                 lambda: ops.moe_ep_dispatch(hid, wrong_id, w, k, None, E, 2)):
+        call()
+        assert ops.device_failure(clear=False) == ops.MOE_ERR_DEVICE_CHECK
+        assert kept_failure(ops) == (ops.MOE_ERR_DEVICE_CHECK, ops.MOE_OK)
