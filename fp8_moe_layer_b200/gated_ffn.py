@@ -84,15 +84,31 @@ class GatedFFN(torch.nn.Module):
                                 *ops.moe_quant_int8(self.w2.detach()))
 
 
-class Int8GatedFFN:
-    """A W8A8 int8 SwiGLU FFN: codes w13 [2F, d], w2 [d, F] with scales [2F], [d]; bf16 tokens. It
-    serves: tokens whose gradient is wanted are refused."""
+class Int8GatedFFN(torch.nn.Module):
+    """A W8A8 int8 SwiGLU FFN: codes w13 [2F, d], w2 [d, F] with scales [2F], [d] (buffers that hold them
+    as those of one expert); bf16 tokens. It serves: tokens whose gradient is wanted are refused. Casts
+    of a model leave the scales in fp32."""
 
     def __init__(self, w13, w13_scale, w2, w2_scale):
-        self.weights = tuple(t.unsqueeze(0) for t in (w13, w13_scale, w2, w2_scale))
+        super().__init__()
         self.d, self.F = w2.shape
+        for name, t in zip(("w13", "w13_scale", "w2", "w2_scale"), (w13, w13_scale, w2, w2_scale)):
+            self.register_buffer(name, t.detach().unsqueeze(0))
 
-    def __call__(self, x, dtype=torch.bfloat16):
+    @property
+    def weights(self):
+        return self.w13, self.w13_scale, self.w2, self.w2_scale
+
+    def _apply(self, fn, recurse=True):
+        scales = {n: getattr(self, n) for n in ("w13_scale", "w2_scale")}
+        super()._apply(fn, recurse)
+        for name, scale in scales.items():
+            now = getattr(self, name)
+            if now.dtype != scale.dtype:
+                setattr(self, name, scale.to(now.device))
+        return self
+
+    def forward(self, x, dtype=torch.bfloat16):
         """y [..., d] of x [..., d] bf16, summed in fp32 and rounded once to ``dtype``."""
         ops._no_derivative("Int8GatedFFN", x)
         rows = x.reshape(-1, x.shape[-1]).contiguous()

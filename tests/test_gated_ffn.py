@@ -91,3 +91,28 @@ def test_int8_layers_refuse_inputs_whose_derivative_is_wanted(int8_call):
         assert int8_call(leaf).shape == (5, 64)
     with forward_ad.dual_level(), torch.no_grad(), pytest.raises(NotImplementedError):
         int8_call(forward_ad.make_dual(x, x))
+
+
+def test_int8_block_is_a_module(gffn):
+    """It takes the 16-bit block's place in a model, moves with it, and saves and loads with it."""
+    class Layer(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.ffn = gffn.GatedFFN(64, 32, device="cpu")
+
+    q = [t[0] for t in int8_weights(1, 64, 32)]
+    q[0][3], q[1][5] = 7, 0.25
+    layer = Layer()
+    layer.ffn = gffn.Int8GatedFFN(*q)
+    assert not list(layer.parameters())
+    state = layer.state_dict()
+    assert sorted(state) == ["ffn.w13", "ffn.w13_scale", "ffn.w2", "ffn.w2_scale"]
+    other = Layer()
+    other.ffn = gffn.Int8GatedFFN(*(t[0] for t in int8_weights(1, 64, 32)))
+    other.load_state_dict(state)
+    for moved in (other, other.to(torch.bfloat16), other.half(), other.double(), other.to("cpu").float()):
+        for t, want in zip(moved.ffn.weights, q):
+            assert t.dtype == want.dtype and torch.equal(t[0], want)
+    meta = other.to("meta")
+    assert all(t.device.type == "meta" for t in meta.ffn.weights)
+    assert [t.dtype for t in meta.ffn.weights] == [t.dtype for t in q]
