@@ -280,7 +280,7 @@ def moe_grouped_ffn_int8(hidden, w13, w13_scale, w2, w2_scale, expert_offsets, p
         raise TypeError(f"perm_token must be int32 on {dev}")
     if perm_token.numel() < T * k_max or not perm_token.is_contiguous():
         raise ValueError("perm_token must be contiguous and hold T * k_max rows")
-    ws = alloc_workspace(dm, dev) if ws is None else ws
+    ws = alloc_workspace(dm, dev) if ws is None else _own_workspace(ws, dev)
     out = torch.empty(max(T * k_max, 1), d, dtype=torch.float32, device=dev)
     if T == 0:
         out.zero_()
@@ -427,8 +427,13 @@ def _workspace(ws: Optional[torch.Tensor], need: int, where: str, device) -> tor
         raise MoEError(MOE_ERR_INVALID_ARG, where)
     if ws is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    if ws.dtype != torch.uint8 or ws.device != device:
-        raise ValueError(f"ws must be a uint8 tensor on {device}")
+    return _own_workspace(ws, device)
+
+
+def _own_workspace(ws: torch.Tensor, device) -> torch.Tensor:
+    """A caller's workspace, whose elements have to be its bytes (an expanded one has fewer)."""
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
     return ws
 
 

@@ -116,3 +116,15 @@ def test_int8_block_is_a_module(gffn):
     meta = other.to("meta")
     assert all(t.device.type == "meta" for t in meta.ffn.weights)
     assert [t.dtype for t in meta.ffn.weights] == [t.dtype for t in q]
+
+
+def test_workspaces_that_are_not_their_bytes_are_refused(gffn):
+    """An expanded tensor has as many elements as asked for and a single byte behind them; a workspace of
+    another device is not the kernels' to write."""
+    ops, cpu = gffn.ops, torch.device("cpu")
+    plain = torch.empty(4096, dtype=torch.uint8)
+    assert ops._workspace(plain, 4096, "", cpu) is plain
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(4096), plain[::2], plain.view(torch.int32),
+               torch.empty(4096, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError):
+            ops._workspace(ws, 4096, "", cpu)

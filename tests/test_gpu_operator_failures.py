@@ -234,3 +234,14 @@ def test_failures_of_every_kernel_file_are_kept(ops):
         call()
         assert ops.device_failure(clear=False) == ops.MOE_ERR_DEVICE_CHECK
         assert kept_failure(ops) == (ops.MOE_ERR_DEVICE_CHECK, ops.MOE_OK)
+
+
+def test_expert_workspaces_that_are_not_their_bytes_are_refused(ops):
+    T, d, E, F, k = 9, 144, 4, 80, 2
+    hid, ids, _, q13, s13, q2, s2 = operands(T, d, E, F, k, 1)
+    off, perm, _ = ops.moe_permute(ids, k, None, E, d=d, F=F)
+    need = ops.workspace_bytes(ops.dims(T, d, E, F, k))
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(need),
+               torch.empty(need, dtype=torch.uint8), torch.empty(need, dtype=torch.int8, device="cuda")):
+        with pytest.raises(ValueError):
+            ops.moe_grouped_ffn_int8(hid, q13, s13, q2, s2, off, perm, k, ws=ws)
