@@ -93,7 +93,8 @@ struct DenseCfg {
 
 // tile -> product p, m-tile, n-tile: inside a product, groups of 8 m-tiles with m fastest, so the
 // units running at one time share both operands' rows in L2 (forward pass at T = 8192, d = 7168, F = 2048
-// over seconds: groups of 4, 8, 16, 32: 612, 608, 614, 629 us).
+// over seconds: groups of 32 629 us; 4, 8 and 16 are alike, 612, 608 and 614 in one run, 625, 624 and 624
+// in another).
 __device__ __forceinline__ void dense_tile_at(const DenseArgs& a, int tile, int& p, int& m, int& n) {
   p = 0;
   while (p + 1 < a.n_problems && tile >= a.p[p + 1].tile0) ++p;

@@ -15,7 +15,7 @@
 // in shared memory where they fit (else L2), and the int8 product quantises them there itself while the
 // first turns are on their way.
 //
-// One token, d = 4096, F = 14336 in bf16 (352 MB, both halves): 61 us, 5.8 TB/s (gate/up alone 43 us under
+// One token, d = 4096, F = 14336 in bf16 (352 MB, both halves): 61 us, 5.8 TB/s (gate/up alone 42 us under
 // ncu). Other forms: loads into registers, nothing in flight between a warp's turns, 80 us; a ring filled
 // by one cp.async.bulk per row piece 161 us (about 45 cycles per copy whatever its size); tcgen05 tiles
 // 128 columns wide 297 us, dealt out evenly 70 us.

@@ -456,6 +456,8 @@ static int run_ffn(const Plan& p, const Ws& w, const uint8_t* w13, const float* 
 // Mean rows per expert from which moe_grouped_ffn_int8 uses the routed dense GEMMs. Whole calls, weights
 // as rows against routed: 128 rows (E 8, d 4096, F 14336) 320 : 359 us, 256 rows 488 : 511; 512 rows (E 32,
 // d 7168, F 2048) 921 : 839; 1024 rows (E 8, d 4096, F 4096) 482 : 464, (E 64, d 2048, F 1024) 786 : 683.
+// (The host knows T k_max slots, not how many of them a batch with a per-token k uses: such a batch may
+// come to the routed form with fewer rows than this.)
 constexpr int kRoutedMeanRows = 384;
 
 static int routed_ffn_int8(const Plan& p, const Ws& w, const uint8_t* w13, const float* w13_scale,

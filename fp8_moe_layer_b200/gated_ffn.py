@@ -5,6 +5,8 @@ layer is trained, W8A8 int8 when it is served.
 ``GatedFFN`` holds its two weights; ``GatedFFN.to_int8`` quantises their rows
 (``ops.moe_quant_int8``) for ``Int8GatedFFN``, which runs the routed int8 experts with one expert
 (``ops.moe_grouped_ffn_int8``).
+
+All three take their workspaces for one call; ``ops.device_failure`` tells whether a kernel gave up a wait.
 """
 from __future__ import annotations
 
@@ -40,7 +42,7 @@ class _GatedFFN(torch.autograd.Function):
 def gated_ffn(x, w13, w2, activation: str = "silu"):
     """(act(x Wg^T) * (x Wu^T)) W2^T for x [..., d] in bf16 or fp16, with first-order reverse-mode
     gradients for x, w13 [2F, d] and w2 [d, F]; tensors that carry a forward-mode tangent are refused.
-    The pre-activations are kept for the backward pass when one of them asks for a gradient. (Capturing
+    Tokens and weights have one type, under ``torch.autocast`` too. The pre-activations are kept for the backward pass when one of them asks for a gradient. (Capturing
     the backward pass into a CUDA graph follows torch's rule: no eager graph of the same leaves may be
     alive during the capture.)"""
     # (a dual tensor need not require a gradient: without a word its tangent would come back as none,

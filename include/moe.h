@@ -33,7 +33,8 @@
  *     (shapes, NULL pointers, alignment, workspace size, unsupported device) and nothing is
  *     launched. MOE_ERR_CUDA reports a failed launch. Errors detected on the device (an index out
  *     of range in caller-provided routing data, a bounded wait that expired) are recorded in a
- *     status word inside `ws` and read with moe_device_status; the kernels never trap.
+ *     status word inside `ws` and read with moe_device_status; the kernels never trap. The first
+ *     such error on a device is also kept apart from any workspace (moe_failures.h).
  *   - T == 0 is valid and launches nothing.
  */
 #ifndef FP8_MOE_H

@@ -7,7 +7,9 @@
  * The conventions of moe.h hold: device pointers, dense row-major tensors, 16-byte alignment where
  * noted, a caller-owned workspace of the size asked for (256-byte aligned), asynchronous calls on
  * `stream`, negative moe_status values for what the host can check. Every entry point with a
- * workspace clears its status word first (moe_grouped_ffn_int8 excepted); moe_device_status(ws, ...) reads it after the call.
+ * workspace clears its status word first (moe_grouped_ffn_int8 excepted); moe_device_status(ws, ...) reads
+ * it after the call, and moe_failures.h has the first failure of any call. A call with T == 0 launches no
+ * kernel and leaves the workspace as it is.
  * Calls whose workspaces differ are independent; two calls that may overlap need two workspaces.
  * Outputs must not overlap inputs or each other.
  */
@@ -57,6 +59,8 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
  *   s_t, xq = quantised hidden[t,:];   h[j] = s_t * w13_scale[e,j] * sum_d xq[d] * w13[e,j,d];
  *   act[f] = silu(h[f]) * h[F+f] (fp32);  s2, aq = quantised act over all F;
  *   expert_out[r,i] = s2 * w2_scale[e,i] * sum_f aq[f] * w2[e,i,f]
+ * Unlike moe_matmul_int8's, a sum need not be exact: batches of few tokens split it into up to 32 parts,
+ * whose exact int32 sums become fp32, are scaled and then added in fp32.
  *   w13 [E, 2F, d] int8; w2 [E, d, F] int8; every other argument, the layouts, the workspace
  *   (moe_workspace_bytes) and the errors as for moe_grouped_ffn_fp8; like it, this entry point leaves
  *   the status word as it is. Every row of expert_out is written: rows of no expert (r >= R, or
@@ -83,8 +87,9 @@ size_t moe_gated_ffn_backward_workspace_bytes(const moe_ffn_dims* dims);
  *   x [T, d]; w13 [2F, d] (rows [0, F) gate, [F, 2F) up); w2 [d, F]; out y [T, d];
  *   out h [T, 2F] or NULL: the pre-activations [gate | up], kept for the backward pass.
  * Products accumulate in fp32. act(g) * u is formed in fp32 from the unrounded sums and rounded once
- * to the operands' type (it is an operand of the second product); h and y are rounded once. All
- * tensors are bit patterns of dims->dtype, 16-byte aligned. T == 0 is a no-op. */
+ * to the operands' type (it is an operand of the second product); h and y are rounded once. In fp16 a
+ * value of any of the three beyond 65504 becomes infinite, for its token alone; bf16 has fp32's range.
+ * All tensors are bit patterns of dims->dtype, 16-byte aligned. T == 0 is a no-op. */
 int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w13,
                   const uint16_t* w2, uint16_t* y, uint16_t* h, void* ws, size_t ws_bytes,
                   void* stream);
@@ -93,8 +98,8 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
  *   da = dy W2;  dh = [da * u * act'(g) | da * act(g)]  with [g | u] = h;
  *   dx = dh W13 [T, d];  dw13 = dh^T x [2F, d];  dw2 = dy^T (act(g) * u) [d, F].
  * Any of dx, dw13, dw2 may be NULL and is then not computed (x may be NULL without dw13, w13 without
- * dx). Products accumulate in fp32; dh and act(g) * u are rounded once to the operands' type, da is
- * not rounded, and each gradient is rounded once. T == 0 writes zeros to dw13 and dw2. */
+ * dx). Products accumulate in fp32; dh and act(g) * u are rounded once to the operands' type (with
+ * fp16's range, as above), da is not rounded, and each gradient is rounded once. T == 0 writes zeros to dw13 and dw2. */
 int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const uint16_t* x,
                            const uint16_t* w13, const uint16_t* w2, const uint16_t* h,
                            uint16_t* dx, uint16_t* dw13, uint16_t* dw2, void* ws, size_t ws_bytes,
