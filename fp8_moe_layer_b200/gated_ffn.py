@@ -42,9 +42,9 @@ class _GatedFFN(torch.autograd.Function):
 def gated_ffn(x, w13, w2, activation: str = "silu"):
     """(act(x Wg^T) * (x Wu^T)) W2^T for x [..., d] in bf16 or fp16, with first-order reverse-mode
     gradients for x, w13 [2F, d] and w2 [d, F]; tensors that carry a forward-mode tangent are refused.
-    Tokens and weights have one type, under ``torch.autocast`` too. The pre-activations are kept for the backward pass when one of them asks for a gradient. (Capturing
-    the backward pass into a CUDA graph follows torch's rule: no eager graph of the same leaves may be
-    alive during the capture.)"""
+    Tokens and weights have one type, under ``torch.autocast`` too. The pre-activations are kept for the
+    backward pass when one of them asks for a gradient. (Capturing the backward pass into a CUDA graph
+    follows torch's rule: no eager graph of the same leaves may be alive during the capture.)"""
     # (a dual tensor need not require a gradient: without a word its tangent would come back as none,
     # which stands for a derivative of zero)
     if any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w13, w2)):
