@@ -199,9 +199,13 @@ __global__ void __launch_bounds__(256) reduce_splits_kernel(const float* __restr
                                                             float* __restrict__ out) {
   pdl_wait();      // predecessor kernel complete, its writes visible
   pdl_trigger();   // let the next kernel launch
-  const int R0 = max(offsets[0], 0), R = tiles[E] > 0 ? (int)min((int64_t)offsets[E], rcap) : 0;
+  const int first = offsets[0], end = offsets[E], any = tiles[E];
+  const int R0 = max(first, 0), R = any > 0 ? (int)min((int64_t)max(end, 0), rcap) : 0;
   const int nv = d / 4;
-  for (int r = R0 + blockIdx.x; r < R; r += gridDim.x) {
+  // (counted from 0: with rows from R0 + blockIdx.x on the compiler keeps fewer partial sums in flight, one
+  // token at d = 4096, F = 14336 60 us a call instead of 56)
+  for (int r = blockIdx.x; r < R; r += gridDim.x) {
+    if (r < R0) continue;
     for (int i = threadIdx.x; i < nv; i += blockDim.x) {
       float4 v = reinterpret_cast<const float4*>(o + (size_t)r * d)[i];
       for (int s = 1; s < splits; ++s) {
