@@ -505,7 +505,9 @@ static int grouped_ffn(bool int8, const moe_dims* dims, const uint16_t* hidden, 
   if (!hidden || !w13 || !w13_scale || !w2 || !w2_scale || !expert_offsets || !perm_token ||
       !expert_out)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(hidden, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(expert_out, 16))
+  if (!aligned(hidden, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(expert_out, 16) ||
+      !aligned(w13_scale, 4) || !aligned(w2_scale, 4) || !aligned(expert_offsets, 4) ||
+      !aligned(perm_token, 4) || !aligned(act_scale_out, 4))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(p, ws, ws_bytes));
   MOE_TRY(check_device());
