@@ -66,8 +66,8 @@ cudaError_t launch_quant_int8(int64_t rows, int K, int type, const void* x, int8
 // Offsets that are out of order zero the whole output. For few rows a block quantises
 // hidden[perm[r]] straight into row r (no launch for the tokens' codes). For many (COPY), a token is
 // quantised once and its codes are copied by a warp per row, which is 1 % of the call faster than
-// quantising it k times (Qwen3 shape, T = 4096, k = 8: 408 against 412 us), and reads hidden once. An index outside [0, T) gives a zero row and flags
-// MOE_ERR_DEVICE_CHECK.
+// quantising it k times (Qwen3 shape, T = 4096, k = 8: 408 against 412 us), and reads hidden once. An
+// index outside [0, T) gives a zero row and flags MOE_ERR_DEVICE_CHECK.
 template <bool COPY>
 __global__ void __launch_bounds__(256) int8_prepare_kernel(const Int8Prepare a) {
   pdl_wait();      // predecessor kernel complete, its writes visible

@@ -59,8 +59,8 @@ int moe_matmul_int8(int32_t T, int32_t N, int32_t K, int32_t x_type, const void*
  *   s_t, xq = quantised hidden[t,:];   h[j] = s_t * w13_scale[e,j] * sum_d xq[d] * w13[e,j,d];
  *   act[f] = silu(h[f]) * h[F+f] (fp32);  s2, aq = quantised act over all F;
  *   expert_out[r,i] = s2 * w2_scale[e,i] * sum_f aq[f] * w2[e,i,f]
- * Unlike moe_matmul_int8's, a sum need not be exact: batches of few tokens split it into up to 32 parts,
- * whose exact int32 sums become fp32, are scaled and then added in fp32.
+ * Unlike moe_matmul_int8's, a sum need not be exact: a product of few tiles splits its contraction into
+ * up to 32 parts, whose exact int32 sums become fp32, are scaled and then added in fp32.
  *   w13 [E, 2F, d] int8; w2 [E, d, F] int8; every other argument, the layouts, the workspace
  *   (moe_workspace_bytes) and the errors as for moe_grouped_ffn_fp8; like it, this entry point leaves
  *   the status word as it is. Every row of expert_out is written: rows of no expert (r >= R, or
@@ -99,7 +99,8 @@ int moe_gated_ffn(const moe_ffn_dims* dims, const uint16_t* x, const uint16_t* w
  *   dx = dh W13 [T, d];  dw13 = dh^T x [2F, d];  dw2 = dy^T (act(g) * u) [d, F].
  * Any of dx, dw13, dw2 may be NULL and is then not computed (x may be NULL without dw13, w13 without
  * dx). Products accumulate in fp32; dh and act(g) * u are rounded once to the operands' type (with
- * fp16's range, as above), da is not rounded, and each gradient is rounded once. T == 0 writes zeros to dw13 and dw2. */
+ * fp16's range, as above), da is not rounded, and each gradient is rounded once. T == 0 writes zeros
+ * to dw13 and dw2. */
 int moe_gated_ffn_backward(const moe_ffn_dims* dims, const uint16_t* dy, const uint16_t* x,
                            const uint16_t* w13, const uint16_t* w2, const uint16_t* h,
                            uint16_t* dx, uint16_t* dw13, uint16_t* dw2, void* ws, size_t ws_bytes,

@@ -19,10 +19,11 @@ extern "C" {
 #endif
 
 /* Host only. When `on` is non-zero, every CTA of the gate/up GEMM launched by the following
- * moe_forward / moe_grouped_ffn_fp8 / moe_grouped_ffn_int8 calls (mean rows per expert below 384), or of
- * the first GEMM of a moe_gated_ffn (T > 16) or moe_gated_ffn_backward call, issues its first tile's MMAs but withholds the signal
- * that the tile's accumulators are ready. The epilogue warps' bounded wait for that signal then
- * expires (2 ms): they record MOE_ERR_DEVICE_TIMEOUT with where-code 4 (10: a dense GEMM) in the
+ * moe_forward / moe_grouped_ffn_fp8 / moe_grouped_ffn_int8 calls (the last with fewer than 384 slots per
+ * expert), or of the first GEMM of a moe_gated_ffn (T > 16) or moe_gated_ffn_backward call, issues its
+ * first tile's MMAs but withholds the signal that the tile's accumulators are ready. The epilogue
+ * warps' bounded wait for that signal then expires (2 ms): they record MOE_ERR_DEVICE_TIMEOUT with
+ * where-code 4 (gate/up GEMM; 10 for a dense GEMM) in the
  * workspace status word, and every warp of the kernel unwinds through its own bounded waits,
  * lets its in-flight copies and MMAs land, frees its tensor memory and returns. The call itself
  * still returns MOE_OK (the launches succeeded); moe_device_status reports the timeout. Pass 0
